@@ -8,6 +8,7 @@ the call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -24,11 +25,12 @@ LIB_ENV = "GDR_LIBRARY"
 GDR_OK, GDR_ERR_INVALID, GDR_ERR_UNSUPPORTED, GDR_ERR_CUDA, GDR_ERR_TIMEOUT, GDR_ERR_BOUNDS = \
     range(6)
 GDR_F32, GDR_BF16 = 0, 1
-GDR_GATE_SCALAR, GDR_GATE_PER_KEY_CHANNEL = 0, 1
+GDR_GATE_SCALAR, GDR_GATE_PER_KEY_CHANNEL, GDR_GATE_HEAD = 0, 1, 2
 PATHS = {"auto": 0, "simt": 1, "tc": 2}
 KERNELS = {"decode": 0, "fwd_simt": 1, "tc_plan": 2, "tc_wy": 3, "tc_state": 4, "gdp_remap": 5,
            "gdn2_simt": 6, "gdn2_decode": 7, "frame_gram": 8, "frame_solve": 9, "frame_chain": 10,
-           "frame_out": 11}
+           "frame_out": 11, "lin_decode": 12, "lin_plan": 13, "lin_state": 14, "lin_scan": 15,
+           "lin_out": 16, "lin_grad": 17, "lin_sum": 18}
 
 _lib = None
 
@@ -86,6 +88,16 @@ def lib() -> ctypes.CDLL:
         L.gdr_fwd_frame_workspace_size.argtypes = [i] * 6
         L.gdr_fwd_frame.restype = i
         L.gdr_fwd_frame.argtypes = [vp] * 8 + [i] * 8 + [vp, sz, vp]
+        L.gdr_fwd_linear_workspace_size.restype = sz
+        L.gdr_fwd_linear_workspace_size.argtypes = [i] * 11
+        L.gdr_fwd_linear.restype = i
+        L.gdr_fwd_linear.argtypes = [vp] * 7 + [i] * 6 + [vp, i, i, i, i, vp, sz, vp]
+        L.gdr_decode_step_linear.restype = i
+        L.gdr_decode_step_linear.argtypes = [vp] * 6 + [i] * 7 + [vp]
+        L.gdr_bwd_linear_workspace_size.restype = sz
+        L.gdr_bwd_linear_workspace_size.argtypes = [i] * 11
+        L.gdr_bwd_linear.restype = i
+        L.gdr_bwd_linear.argtypes = [vp] * 12 + [i] * 6 + [vp, i, i, i, i, vp, sz, vp]
         L.gdr_profile_enable.restype = None
         L.gdr_profile_enable.argtypes = [i]
         L.gdr_profile_read.restype = i
@@ -366,6 +378,164 @@ def gdr_decode_step(q, k, v, g, beta, S, *, out=None, stream=None) -> torch.Tens
     if st != GDR_OK:
         raise GdrError(st, "gdr_decode_step")
     return out
+
+
+@functools.lru_cache(maxsize=1024)
+def fwd_linear_workspace_size(B, T, H, H_k, d_k, d_v, n_seq, varlen, dtype, gate,
+                              path="auto") -> int:
+    return int(lib().gdr_fwd_linear_workspace_size(B, T, H, H_k, d_k, d_v, n_seq,
+                                                   int(bool(varlen)), dtype, gate, PATHS[path]))
+
+
+@functools.lru_cache(maxsize=1024)
+def bwd_linear_workspace_size(B, T, H, H_k, d_k, d_v, n_seq, varlen, dtype, gate,
+                              path="auto") -> int:
+    return int(lib().gdr_bwd_linear_workspace_size(B, T, H, H_k, d_k, d_v, n_seq,
+                                                   int(bool(varlen)), dtype, gate, PATHS[path]))
+
+
+def _linear_args(q, k, v, g, tensors):
+    """Shapes and checks shared by the linear attention calls: q, k
+    [*lead, H_k, d_k], v [*lead, H, d_v], g [*lead, H] or [H]; ``tensors`` are
+    further ``(name, tensor, dtype, shape)``.  Every shape must match, every
+    tensor be contiguous and on q's device."""
+    dev = _on_cuda(q)
+    lead = q.shape[:-2]
+    (H_k, d_k), (H, d_v) = q.shape[-2:], v.shape[-2:]
+    gate = GDR_GATE_HEAD if g.dim() == 1 else GDR_GATE_SCALAR
+    if g.dim() == len(lead) + 2:
+        raise ValueError("linear attention takes one decay per head ([..., H] or [H]), "
+                         "not one per key channel")
+    if H_k < 1 or H % H_k:
+        raise ValueError(f"{H} value heads do not share {H_k} query/key heads evenly")
+    for name, t, dtype, shape in (("q", q, q.dtype, q.shape), ("k", k, q.dtype, q.shape),
+                                  ("v", v, q.dtype, (*lead, H, d_v)),
+                                  ("g", g, torch.float32, (H,) if gate else (*lead, H)), *tensors):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}; expected {dev}")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {tuple(shape)}")
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+    return dev, _dtype_code(q), gate, H, H_k, d_k, d_v
+
+
+def _linear_call(dev, stream, ws_bytes, workspace, shapes, call):
+    """Allocate what ``shapes`` asks for (``(tensor or None, shape or None,
+    dtype)``; given tensors are kept) and the workspace, then run ``call(made,
+    workspace, bytes, stream)`` with ``dev`` current.  Allocations belong to
+    the stream that the kernels run on, so that the allocator hands the
+    workspace to no other stream while they run."""
+    if workspace is not None:
+        _check(dev, ("workspace", workspace, None, 0))
+        _need_contig(workspace)
+    handle = _stream(stream, dev)
+
+    def go():
+        made = [t if t is not None or shape is None else
+                torch.empty(shape, dtype=dtype, device=dev) for t, shape, dtype in shapes]
+        ws, n = workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+        if n < ws_bytes:
+            ws, n = torch.empty(ws_bytes, dtype=torch.uint8, device=dev), ws_bytes
+        return made, call(made, ws, n, handle)
+
+    if stream is not None:
+        s = stream if isinstance(stream, torch.cuda.Stream) else \
+            torch.cuda.ExternalStream(handle.value or 0, device=dev)
+        with torch.cuda.device(dev), torch.cuda.stream(s):
+            return go()
+    if torch.cuda.current_device() == dev.index:
+        return go()
+    return _call_on(dev, go)
+
+
+def _linear_cu(cu_seqlens, B):
+    if cu_seqlens is None:
+        return B, 0
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must be [n_seq + 1]")
+    if B != 1:
+        raise ValueError("a packed batch has B = 1")
+    return cu_seqlens.numel() - 1, 1
+
+
+def gdr_fwd_linear(q, k, v, g, S0=None, *, cu_seqlens=None, out=None, S_final=None,
+                   want_final: bool = True, path: str = "auto", workspace=None,
+                   stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Linear attention with a decay for each head, whole sequences: q, k
+    [B,T,H_k,d_k], v [B,T,H,d_v] (value heads share query/key heads when
+    H_k < H), g [B,T,H] or [H]; returns ``(out [B,T,H,d_v], S_final
+    [N,H,d_v,d_k] or None)``."""
+    B, T = q.shape[:2]
+    n_seq, varlen = _linear_cu(cu_seqlens, B)
+    st_shape = (n_seq, v.shape[-2], v.shape[-1], q.shape[-1])
+    dev, dtype, gate, H, H_k, d_k, d_v = _linear_args(q, k, v, g, (
+        ("S0", S0, torch.float32, st_shape), ("out", out, q.dtype, v.shape),
+        ("S_final", S_final, torch.float32, st_shape),
+        ("cu_seqlens", cu_seqlens, torch.int32, (n_seq + 1,))))
+    need = fwd_linear_workspace_size(B, T, H, H_k, d_k, d_v, n_seq, varlen, dtype, gate, path)
+    (out, S_final), st = _linear_call(
+        dev, stream, need, workspace,
+        ((out, v.shape, q.dtype), (S_final, st_shape if want_final else None, torch.float32)),
+        lambda made, ws, n, s: lib().gdr_fwd_linear(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S0), _ptr(made[0]), _ptr(made[1]), B, T, H, H_k,
+            d_k, d_v, _ptr(cu_seqlens), n_seq, dtype, gate, PATHS[path], _ptr(ws), n, s))
+    if st != GDR_OK:
+        raise GdrError(st, "gdr_fwd_linear")
+    return out, S_final
+
+
+def gdr_decode_step_linear(q, k, v, g, S, *, out=None, stream=None) -> torch.Tensor:
+    """Linear attention decode of one token per sequence, updating ``S``
+    [N,H,d_v,d_k] in place: q, k [N,H_k,d_k], v [N,H,d_v], g [N,H] or [H];
+    returns out [N,H,d_v]."""
+    N = q.shape[0]
+    dev, dtype, gate, H, H_k, d_k, d_v = _linear_args(q, k, v, g, (
+        ("S", S, torch.float32, (N, v.shape[-2], v.shape[-1], q.shape[-1])),
+        ("out", out, q.dtype, v.shape)))
+    (out,), st = _linear_call(
+        dev, stream, 0, None, ((out, v.shape, q.dtype),),
+        lambda made, ws, n, s: lib().gdr_decode_step_linear(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S), _ptr(made[0]), N, H, H_k, d_k, d_v, dtype,
+            gate, s))
+    if st != GDR_OK:
+        raise GdrError(st, "gdr_decode_step_linear")
+    return out
+
+
+def gdr_bwd_linear(q, k, v, g, dout, S0=None, dS_final=None, *, cu_seqlens=None, dq=None, dk=None,
+                   dv=None, dg=None, dS0=None, want_dS0: bool = True, path: str = "auto",
+                   workspace=None, stream=None):
+    """Gradients of gdr_fwd_linear from ``dout`` [B,T,H,d_v] and ``dS_final``
+    [N,H,d_v,d_k] (None: zero); returns ``(dq, dk, dv, dg, dS0 or None)``,
+    dq, dk and dv of the tokens' type, dg and dS0 fp32."""
+    B, T = q.shape[:2]
+    n_seq, varlen = _linear_cu(cu_seqlens, B)
+    st_shape = (n_seq, v.shape[-2], v.shape[-1], q.shape[-1])
+    f32 = torch.float32
+    dev, dtype, gate, H, H_k, d_k, d_v = _linear_args(q, k, v, g, (
+        ("dout", dout, q.dtype, v.shape), ("S0", S0, f32, st_shape),
+        ("dS_final", dS_final, f32, st_shape), ("dq", dq, q.dtype, q.shape),
+        ("dk", dk, q.dtype, q.shape), ("dv", dv, q.dtype, v.shape), ("dg", dg, f32, g.shape),
+        ("dS0", dS0, f32, st_shape), ("cu_seqlens", cu_seqlens, torch.int32, (n_seq + 1,))))
+    need = bwd_linear_workspace_size(B, T, H, H_k, d_k, d_v, n_seq, varlen, dtype, gate, path)
+    made, st = _linear_call(
+        dev, stream, need, workspace,
+        ((dq, q.shape, q.dtype), (dk, q.shape, q.dtype), (dv, v.shape, q.dtype), (dg, g.shape, f32),
+         (dS0, st_shape if want_dS0 else None, f32)),
+        lambda made, ws, n, s: lib().gdr_bwd_linear(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S0), _ptr(dout), _ptr(dS_final),
+            *(_ptr(t) for t in made), B, T, H, H_k, d_k, d_v, _ptr(cu_seqlens), n_seq, dtype, gate,
+            PATHS[path], _ptr(ws), n, s))
+    if st != GDR_OK:
+        raise GdrError(st, "gdr_bwd_linear")
+    return tuple(made)
 
 
 def device_status(stream=None) -> int:

@@ -1,0 +1,82 @@
+// Shared pieces of the linear attention kernels (linear.cu, linear_simt.cu,
+// linear_tc.cu): the cut of the sequences into blocks, and the decays.
+//
+// A sequence is cut into blocks of L tokens (the last may be shorter).  A slot
+// is one (sequence, block) pair; the states that enter the blocks are held per
+// (slot, head) as fp32 [d_v, d_k], like S itself.
+#pragma once
+
+#include "common.cuh"
+
+namespace gdr {
+namespace lin {
+
+struct Geo {
+    int T, H, Hk, n_seq, varlen, rows;  // rows: tokens of the whole batch
+    int L, nb, n_slots;                 // nb: blocks per sequence (equal lengths)
+    int gate_head;                      // g is [H]: one log-decay for all tokens
+};
+
+// {first row, tokens, sequence, block}; a slot that no block fills has no tokens.
+struct Plan {
+    const int4 *slot;      // packed batches only
+    const int *blk_start;  // [n_seq + 1]: first slot of each sequence
+};
+
+__device__ __forceinline__ int4 slot_of(const Geo &geo, const Plan &plan, int slot) {
+    if (geo.varlen) return plan.slot[slot];
+    const int s = slot / geo.nb, b = slot - s * geo.nb;
+    return make_int4(s * geo.T + b * geo.L, min(geo.L, geo.T - b * geo.L), s, b);
+}
+
+// A decay of e^-104 is 0 in fp32 (the smallest subnormal is 2^-149 = e^-103.3),
+// so clamping there changes no result and keeps sums of decays finite.
+__device__ __forceinline__ float clamp_g(float g) { return g < -104.f ? -104.f : g; }
+
+__device__ __forceinline__ float load_g(const Geo &geo, const float *g, long row, int h) {
+    return clamp_g(geo.gate_head ? g[h] : g[row * geo.H + h]);
+}
+
+}  // namespace lin
+}  // namespace gdr
+
+namespace gdr_host {
+// Arguments of one call, checked by the entry point.
+struct LinCall {
+    const void *q, *k, *v, *dout;
+    const float *g, *S0, *dS_final;
+    void *out, *dq, *dk, *dv;
+    float *S_final, *dg, *dS0;
+    const int32_t *cu;
+    int B, T, H, Hk, dk_, dv_, n_seq;
+    gdr_dtype dtype;
+    gdr_gate gate;
+    uint8_t *ws;
+    unsigned int *err;
+    cudaStream_t st;
+};
+
+// Byte offsets of the workspace (one layout for the forward and the backward call).
+struct LinWs {
+    size_t slot, blk_start, gtot, gtot_head, X, Y, fin, rdot, cdot, dq32, dk32, part, total;
+    int n_slots, nb, L;
+};
+LinWs lin_ws(int B, int T, int H, int Hk, int dk, int dv, int n_seq, bool varlen, bool bwd, int L,
+             int dot_cols);
+gdr::lin::Geo lin_geo(const LinCall &c, const LinWs &w);
+cudaError_t lin_plan(const LinCall &c, const gdr::lin::Geo &geo, const LinWs &w);
+// States of the blocks carried over each sequence: X[slot] (the block's own
+// contribution) becomes the state that enters the block; forward in time from
+// `init`, or backward (rev).  `fin` (may be NULL) receives the last state.
+cudaError_t lin_scan(const LinCall &c, const gdr::lin::Geo &geo, const LinWs &w, float *X,
+                     const float *init, float *fin, bool rev);
+cudaError_t lin_group_sum(const LinCall &c, const gdr::lin::Geo &geo, const LinWs &w,
+                          const float *x, void *out, int d);
+cudaError_t lin_dg_heads(const LinCall &c, const gdr::lin::Geo &geo, const float *part);
+
+// CUDA-core path (linear_simt.cu)
+constexpr int kLinSimtL = 256;
+cudaError_t lin_fwd_simt(const LinCall &c);
+cudaError_t lin_bwd_simt(const LinCall &c);
+size_t lin_simt_ws_bytes(const LinCall &c, bool bwd);
+}  // namespace gdr_host

@@ -51,7 +51,9 @@ typedef enum {
 
 typedef enum { GDR_F32 = 0, GDR_BF16 = 1 } gdr_dtype;
 
-typedef enum { GDR_GATE_SCALAR = 0, GDR_GATE_PER_KEY_CHANNEL = 1 } gdr_gate;
+/* GDR_GATE_HEAD (one log-decay per head, for all tokens) is taken by the linear
+ * attention entry points only. */
+typedef enum { GDR_GATE_SCALAR = 0, GDR_GATE_PER_KEY_CHANNEL = 1, GDR_GATE_HEAD = 2 } gdr_gate;
 
 /* Which kernels run the prefill.
  *  GDR_PATH_AUTO        tensor-core path when it applies (bf16, d_k = d_v = 128,
@@ -274,6 +276,65 @@ gdr_status gdr_fwd_frame(const void *q, const void *k, const void *v, const floa
                          void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Linear attention with a decay for each head: the recurrence of this library
+ * without the delta correction ("Linear Attention, Visualized", sections
+ * "RetNet" and "Mamba-2"; the beta -> 0 limit of the gated delta rule's
+ * transition with an undamped write):
+ *
+ *     S_t = e^{g_t} S_{t-1} + v_t k_t^T,    o_t = S_t q_t.
+ *
+ * Value heads may share query/key heads: value head h reads query/key head
+ * h / (H / H_k), H a multiple of H_k.  The decay is GDR_GATE_SCALAR (one per
+ * token and value head) or GDR_GATE_HEAD (one per value head, the same for
+ * every token: RetNet); GDR_GATE_PER_KEY_CHANNEL is GDR_ERR_UNSUPPORTED.
+ * A log-decay below -104 (-inf included) is a decay of exactly 0 in fp32: the
+ * state is forgotten.
+ *
+ * gdr_fwd_linear: whole sequences.
+ *  q, k     [B, T, H_k, d_k]  dtype;   v, out  [B, T, H, d_v]  dtype
+ *  g        [B, T, H] (GDR_GATE_SCALAR) or [H] (GDR_GATE_HEAD), fp32
+ *  S0, S_final  [N, H, d_v, d_k] fp32 or NULL, cu_seqlens, n_seq, path,
+ *           workspace: as for gdr_fwd.  Offsets that decrease or leave [0, T]
+ *           are taken as their running maximum inside [0, T]; rows that belong
+ *           to no sequence are not written.
+ *  d_k, d_v multiples of 16 in [16, 128].  The tensor-core path takes bf16;
+ *           fp32 tokens run on the CUDA cores.  S_final keeps fp32 accuracy
+ *           on either path.
+ * gdr_decode_step_linear: one token per sequence, in place on S_inout.
+ *  q, k [N, H_k, d_k]; v, out [N, H, d_v]; g [N, H] or [H]; S_inout
+ *  [N, H, d_v, d_k]; the same d_k, d_v.
+ * gdr_bwd_linear: the gradient of gdr_fwd_linear.
+ *  dout     [B, T, H, d_v]    dtype, gradient of out
+ *  dS_final [N, H, d_v, d_k]  fp32, gradient of S_final, or NULL (zero)
+ *  dq, dk   [B, T, H_k, d_k]  dtype (summed in fp32 over the value heads that
+ *           share a query/key head, then rounded once); dv [B, T, H, d_v] dtype
+ *  dg       as g, fp32 (GDR_GATE_HEAD: summed over all tokens)
+ *  dS0      [N, H, d_v, d_k]  fp32, gradient of S0, or NULL to skip
+ *  dg and dS0 keep fp32 accuracy on either path.  No atomics: results do not
+ *  change from run to run.
+ * The *_workspace_size functions return the bytes of device workspace (256-byte
+ * aligned), 0 for arguments the call would reject.
+ */
+size_t gdr_fwd_linear_workspace_size(int B, int T, int H, int H_k, int d_k, int d_v, int n_seq,
+                                     int varlen, gdr_dtype dtype, gdr_gate gate, gdr_path path);
+gdr_status gdr_fwd_linear(const void *q, const void *k, const void *v, const float *g,
+                          const float *S0, void *out, float *S_final, int B, int T, int H,
+                          int H_k, int d_k, int d_v, const int32_t *cu_seqlens, int n_seq,
+                          gdr_dtype dtype, gdr_gate gate, gdr_path path, void *workspace,
+                          size_t workspace_bytes, void *stream);
+gdr_status gdr_decode_step_linear(const void *q, const void *k, const void *v, const float *g,
+                                  float *S_inout, void *out, int N, int H, int H_k, int d_k,
+                                  int d_v, gdr_dtype dtype, gdr_gate gate, void *stream);
+size_t gdr_bwd_linear_workspace_size(int B, int T, int H, int H_k, int d_k, int d_v, int n_seq,
+                                     int varlen, gdr_dtype dtype, gdr_gate gate, gdr_path path);
+gdr_status gdr_bwd_linear(const void *q, const void *k, const void *v, const float *g,
+                          const float *S0, const void *dout, const float *dS_final, void *dq,
+                          void *dk, void *dv, float *dg, float *dS0, int B, int T, int H, int H_k,
+                          int d_k, int d_v, const int32_t *cu_seqlens, int n_seq, gdr_dtype dtype,
+                          gdr_gate gate, gdr_path path, void *workspace, size_t workspace_bytes,
+                          void *stream);
+
+/*
  * gdr_fwd_noalloc -- the prefill for callers that cannot allocate device
  * memory at call time (their memory manager owns the whole device heap and
  * forbids further cudaMalloc, or an allocation's device synchronisation is not
@@ -324,7 +385,11 @@ float gdr_set_gram_spread_limit(float limit);
  * GDR_K_TC_STATE, GDR_K_GDP_REMAP (the Gated DeltaProduct expand/gather),
  * GDR_K_GDN2_SIMT and GDR_K_GDN2_DECODE (Gated DeltaNet-2), GDR_K_FRAME_GRAM,
  * GDR_K_FRAME_SOLVE, GDR_K_FRAME_CHAIN and GDR_K_FRAME_OUT (the implicit frame
- * update's passes).  Launches are always counted.  While timing is enabled,
+ * update's passes), GDR_K_LIN_DECODE, GDR_K_LIN_PLAN (packed batches),
+ * GDR_K_LIN_STATE (states of blocks of tokens), GDR_K_LIN_SCAN (states carried
+ * over the blocks), GDR_K_LIN_OUT (outputs), GDR_K_LIN_GRAD (gradients) and
+ * GDR_K_LIN_SUM (sums over shared heads and over tokens) of linear attention.
+ * Launches are always counted.  While timing is enabled,
  * every launch is bracketed by two CUDA events recorded on the launch's own
  * stream.  gdr_profile_read waits for the recorded events, returns the
  * launches and the summed device time (ms) of kernel `id` since the last read
@@ -334,7 +399,8 @@ float gdr_set_gram_spread_limit(float limit);
 enum { GDR_K_DECODE = 0, GDR_K_FWD_SIMT = 1, GDR_K_TC_PLAN = 2, GDR_K_TC_WY = 3,
        GDR_K_TC_STATE = 4, GDR_K_GDP_REMAP = 5, GDR_K_GDN2_SIMT = 6, GDR_K_GDN2_DECODE = 7,
        GDR_K_FRAME_GRAM = 8, GDR_K_FRAME_SOLVE = 9, GDR_K_FRAME_CHAIN = 10, GDR_K_FRAME_OUT = 11,
-       GDR_K_COUNT = 12 };
+       GDR_K_LIN_DECODE = 12, GDR_K_LIN_PLAN = 13, GDR_K_LIN_STATE = 14, GDR_K_LIN_SCAN = 15,
+       GDR_K_LIN_OUT = 16, GDR_K_LIN_GRAD = 17, GDR_K_LIN_SUM = 18, GDR_K_COUNT = 19 };
 void gdr_profile_enable(int on);
 gdr_status gdr_profile_read(int id, long long *launches, double *total_ms);
 
