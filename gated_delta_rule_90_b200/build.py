@@ -18,7 +18,7 @@ LIB = os.path.join(HERE, "libgdr.so")
 BUILD_CHECK = os.path.join(HERE, "_build_check")
 LIB_CHECK = os.path.join(HERE, "libgdr_check.so")
 SOURCES = ["gdr_api.cu", "decode.cu", "fwd_simt.cu", "fwd_tc.cu", "fwd_noalloc.cu", "product.cu",
-           "frame.cu", "linear.cu", "linear_simt.cu"]
+           "frame.cu", "linear.cu", "linear_simt.cu", "linear_tc.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
          "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC, "--expt-relaxed-constexpr"]

@@ -47,7 +47,7 @@ plan_kernel(const int32_t *__restrict__ cu, Geo geo, int4 *__restrict__ slot,
         int top, add;
         const int m = max(block_scan<true>(max(a, b), wt, &top), hi);
         const int t0 = max(m, a), t1 = max(t0, b);
-        const int n = s < geo.n_seq ? (t1 - t0 + geo.L - 1) / geo.L : 0;
+        const int n = s < geo.n_seq ? max((t1 - t0 + geo.L - 1) / geo.L, geo.keep_empty) : 0;
         const int at = nblk + block_scan<false>(n, wt, &add);
         if (s < geo.n_seq) {
             blk_start[s] = at;
@@ -60,7 +60,7 @@ plan_kernel(const int32_t *__restrict__ cu, Geo geo, int4 *__restrict__ slot,
     if (tid == 0) blk_start[geo.n_seq] = nblk;
     __syncthreads();  // blk_start and start are read by other threads of this CTA below
     for (int i = tid; i < geo.n_slots; i += 1024) {
-        int4 r = make_int4(0, 0, 0, 0);
+        int4 r = make_int4(0, -1, 0, 0);
         if (i < nblk) {
             int lo = 0, up = geo.n_seq - 1;  // the last sequence with blk_start <= i
             while (lo < up) {
@@ -268,10 +268,9 @@ gdr_status check_shapes(int B, int T, int H, int Hk, int dk, int dv, int n_seq, 
 }
 
 // Does the call run on the tensor cores?
-gdr_status resolve(gdr_dtype dtype, gdr_path path, bool *tc) {
-    *tc = false;
-    (void)dtype;
-    return path == GDR_PATH_TENSORCORE ? GDR_ERR_UNSUPPORTED : GDR_OK;
+gdr_status resolve(int T, gdr_dtype dtype, gdr_path path, bool *tc) {
+    *tc = dtype == GDR_BF16 && path != GDR_PATH_SIMT && T > 0;
+    return path == GDR_PATH_TENSORCORE && dtype != GDR_BF16 ? GDR_ERR_UNSUPPORTED : GDR_OK;
 }
 
 template <typename T, int VPL, int LPR>
@@ -335,7 +334,7 @@ LinWs lin_ws(int B, int T, int H, int Hk, int dk, int dv, int n_seq, bool varlen
 }
 
 Geo lin_geo(const LinCall &c, const LinWs &w) {
-    Geo g;
+    Geo g{};
     g.T = c.T; g.H = c.H; g.Hk = c.Hk; g.n_seq = c.cu ? c.n_seq : c.B; g.varlen = c.cu != nullptr;
     g.rows = c.B * c.T; g.L = w.L; g.nb = w.nb; g.n_slots = w.n_slots;
     g.gate_head = c.gate == GDR_GATE_HEAD;
@@ -397,26 +396,26 @@ size_t gdr_fwd_linear_workspace_size(int B, int T, int H, int H_k, int d_k, int 
                                      int varlen, gdr_dtype dtype, gdr_gate gate, gdr_path path) {
     bool tc;
     if (check_shapes(B, T, H, H_k, d_k, d_v, n_seq, varlen != 0, dtype, gate, path) != GDR_OK ||
-        resolve(dtype, path, &tc) != GDR_OK)
+        resolve(T, dtype, path, &tc) != GDR_OK)
         return 0;
     LinCall c{};
     static const int32_t packed = 0;  // only whether cu is NULL matters here
     c.cu = varlen ? &packed : nullptr;
     c.B = B; c.T = T; c.H = H; c.Hk = H_k; c.dk_ = d_k; c.dv_ = d_v; c.n_seq = n_seq;
-    return gdr_host::lin_simt_ws_bytes(c, false);
+    return tc ? gdr_host::lin_tc_ws_bytes(c, false) : gdr_host::lin_simt_ws_bytes(c, false);
 }
 
 size_t gdr_bwd_linear_workspace_size(int B, int T, int H, int H_k, int d_k, int d_v, int n_seq,
                                      int varlen, gdr_dtype dtype, gdr_gate gate, gdr_path path) {
     bool tc;
     if (check_shapes(B, T, H, H_k, d_k, d_v, n_seq, varlen != 0, dtype, gate, path) != GDR_OK ||
-        resolve(dtype, path, &tc) != GDR_OK)
+        resolve(T, dtype, path, &tc) != GDR_OK)
         return 0;
     LinCall c{};
     static const int32_t packed = 0;
     c.cu = varlen ? &packed : nullptr;
     c.B = B; c.T = T; c.H = H; c.Hk = H_k; c.dk_ = d_k; c.dv_ = d_v; c.n_seq = n_seq;
-    return gdr_host::lin_simt_ws_bytes(c, true);
+    return tc ? gdr_host::lin_tc_ws_bytes(c, true) : gdr_host::lin_simt_ws_bytes(c, true);
 }
 
 gdr_status gdr_fwd_linear(const void *q, const void *k, const void *v, const float *g,
@@ -433,18 +432,18 @@ gdr_status gdr_fwd_linear(const void *q, const void *k, const void *v, const flo
                                  path);
     if (st != GDR_OK) return st;
     bool tc = false;
-    if ((st = resolve(dtype, path, &tc)) != GDR_OK) return st;
+    if ((st = resolve(T, dtype, path, &tc)) != GDR_OK) return st;
     LinCall c{};
     c.q = q; c.k = k; c.v = v; c.g = g; c.S0 = S0; c.out = out; c.S_final = S_final;
     c.cu = cu_seqlens; c.B = B; c.T = T; c.H = H; c.Hk = H_k; c.dk_ = d_k; c.dv_ = d_v;
     c.n_seq = n_seq; c.dtype = dtype; c.gate = gate; c.ws = (uint8_t *)workspace;
     c.st = (cudaStream_t)stream;
-    const size_t need = gdr_host::lin_simt_ws_bytes(c, false);
+    const size_t need = tc ? gdr_host::lin_tc_ws_bytes(c, false) : gdr_host::lin_simt_ws_bytes(c, false);
     if (need && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255u)))
         return GDR_ERR_INVALID;
     c.err = gdr_host::device_error_word();
     if (!c.err) return GDR_ERR_CUDA;
-    return gdr_host::lin_fwd_simt(c) == cudaSuccess ? GDR_OK : GDR_ERR_CUDA;
+    return (tc ? gdr_host::lin_fwd_tc(c) : gdr_host::lin_fwd_simt(c)) == cudaSuccess ? GDR_OK : GDR_ERR_CUDA;
 }
 
 gdr_status gdr_decode_step_linear(const void *q, const void *k, const void *v, const float *g,
@@ -484,19 +483,19 @@ gdr_status gdr_bwd_linear(const void *q, const void *k, const void *v, const flo
                                  path);
     if (st != GDR_OK) return st;
     bool tc = false;
-    if ((st = resolve(dtype, path, &tc)) != GDR_OK) return st;
+    if ((st = resolve(T, dtype, path, &tc)) != GDR_OK) return st;
     LinCall c{};
     c.q = q; c.k = k; c.v = v; c.g = g; c.S0 = S0; c.dout = dout; c.dS_final = dS_final;
     c.dq = dq; c.dk = dk; c.dv = dv; c.dg = dg; c.dS0 = dS0;
     c.cu = cu_seqlens; c.B = B; c.T = T; c.H = H; c.Hk = H_k; c.dk_ = d_k; c.dv_ = d_v;
     c.n_seq = n_seq; c.dtype = dtype; c.gate = gate; c.ws = (uint8_t *)workspace;
     c.st = (cudaStream_t)stream;
-    const size_t need = gdr_host::lin_simt_ws_bytes(c, true);
+    const size_t need = tc ? gdr_host::lin_tc_ws_bytes(c, true) : gdr_host::lin_simt_ws_bytes(c, true);
     if (need && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255u)))
         return GDR_ERR_INVALID;
     c.err = gdr_host::device_error_word();
     if (!c.err) return GDR_ERR_CUDA;
-    return gdr_host::lin_bwd_simt(c) == cudaSuccess ? GDR_OK : GDR_ERR_CUDA;
+    return (tc ? gdr_host::lin_bwd_tc(c) : gdr_host::lin_bwd_simt(c)) == cudaSuccess ? GDR_OK : GDR_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -15,9 +15,10 @@ struct Geo {
     int T, H, Hk, n_seq, varlen, rows;  // rows: tokens of the whole batch
     int L, nb, n_slots;                 // nb: blocks per sequence (equal lengths)
     int gate_head;                      // g is [H]: one log-decay for all tokens
+    int keep_empty;                     // an empty packed sequence has one block of no tokens
 };
 
-// {first row, tokens, sequence, block}; a slot that no block fills has no tokens.
+// {first row, tokens, sequence, block}; a slot that no block fills has -1 tokens.
 struct Plan {
     const int4 *slot;      // packed batches only
     const int *blk_start;  // [n_seq + 1]: first slot of each sequence
@@ -79,4 +80,9 @@ constexpr int kLinSimtL = 256;
 cudaError_t lin_fwd_simt(const LinCall &c);
 cudaError_t lin_bwd_simt(const LinCall &c);
 size_t lin_simt_ws_bytes(const LinCall &c, bool bwd);
+
+// tensor-core path (linear_tc.cu)
+cudaError_t lin_fwd_tc(const LinCall &c);
+cudaError_t lin_bwd_tc(const LinCall &c);
+size_t lin_tc_ws_bytes(const LinCall &c, bool bwd);
 }  // namespace gdr_host

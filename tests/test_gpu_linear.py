@@ -69,7 +69,7 @@ def d64(*ts):
     return [None if t is None else t.double() for t in ts]
 
 
-PATHS = [("simt", F32), ("simt", BF)]
+PATHS = [("simt", F32), ("simt", BF), ("tc", BF)]
 # B, T, H, Hk, dk, dv, gate, S0
 SHAPES = [(1, 1, 1, 1, 16, 16, "token", True), (2, 37, 4, 2, 64, 64, "token", True),
           (1, 128, 2, 2, 128, 128, "head", False), (1, 129, 3, 1, 128, 64, "token", True),
