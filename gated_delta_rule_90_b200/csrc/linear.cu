@@ -119,15 +119,18 @@ scan_kernel(float *__restrict__ X, const float *__restrict__ gtot, const float *
 
 // ------------------------------------------------------------ sums
 // The gradient of a shared query/key head: the sum over its value heads, fp32.
+// A CTA takes 16 tokens of a slot.
+constexpr int kSumRows = 16;
 template <typename T>
 __global__ void __launch_bounds__(256)
 group_sum_kernel(const float *__restrict__ x, T *__restrict__ out, Geo geo, Plan plan, int d) {
     // slot by slot, so that rows of no sequence are left as they are
     const int4 sl = slot_of(geo, plan, blockIdx.x);
     const int r = geo.H / geo.Hk, per = geo.Hk * (d / 4);
-    for (long i = threadIdx.x; i < (long)sl.y * per; i += 256) {
-        const long row = sl.x + i / per;
-        const int hk = (int)(i % per) / (d / 4), d4 = (int)(i % per) % (d / 4);
+    const int j0 = blockIdx.y * kSumRows, n = min(kSumRows, sl.y - j0);
+    for (int i = threadIdx.x; i < n * per; i += 256) {
+        const long row = sl.x + j0 + i / per;
+        const int hk = (i % per) / (d / 4), d4 = (i % per) % (d / 4);
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int j = 0; j < r; ++j) {
             const float4 y = *reinterpret_cast<const float4 *>(
@@ -371,12 +374,13 @@ cudaError_t lin_group_sum(const LinCall &c, const Geo &geo, const LinWs &w, cons
                           int d) {
     if (!geo.n_slots) return cudaSuccess;
     const Plan plan = {(const int4 *)(c.ws + w.slot), (const int *)(c.ws + w.blk_start)};
+    const dim3 grid(geo.n_slots, (geo.L + kSumRows - 1) / kSumRows);
     ProfToken tk = prof_begin(GDR_K_LIN_SUM, c.st);
     if (c.dtype == GDR_BF16)
-        group_sum_kernel<__nv_bfloat16><<<geo.n_slots, 256, 0, c.st>>>(x, (__nv_bfloat16 *)out, geo,
+        group_sum_kernel<__nv_bfloat16><<<grid, 256, 0, c.st>>>(x, (__nv_bfloat16 *)out, geo,
                                                                        plan, d);
     else
-        group_sum_kernel<float><<<geo.n_slots, 256, 0, c.st>>>(x, (float *)out, geo, plan, d);
+        group_sum_kernel<float><<<grid, 256, 0, c.st>>>(x, (float *)out, geo, plan, d);
     prof_end(tk, c.st);
     return cudaGetLastError();
 }

@@ -35,18 +35,23 @@ using namespace sm100;
 constexpr int kQ = 128;                  // tokens of a chunk
 constexpr int kN = 64;                   // columns of c of a CTA
 constexpr uint32_t kSpinTc = 1u << 24;   // poll limit of every mbarrier wait
-constexpr int kTcThreads = 384;          // TMA, 2 MMA issuers, decays; 4 output warps; 4 state warps
+constexpr int kTcThreads = 640;          // 8 output warps, 8 state warps, TMA and decays, 3 MMA issuers
+constexpr int kPairThreads = 384;        // TMA, MMA, decays of rows and columns; 4 warps each for their sums
 constexpr uint32_t kAtom = kQ * 128;     // bytes of 128 rows of 64 bf16
 constexpr float kLog2e = 1.4426950408889634f;
 
 enum { kStateOnly = 0, kOut = 1, kOutDots = 2 };
 
-// Shared memory of a CTA.  Buffers of the a, b, c tiles and terms of X by mode:
-// 227 KB hold two of each tile with one term of X; with three terms (32 KB
-// more) a and c have one buffer.
+// Tables of a chunk's decays (floats): LC sums inside each 32-token block in
+// units of log 2, CF column factors, then scalars by block (see decay_tables).
+enum { kLC = 0, kCF = 128, kSS = 256, kSE = 260, kBB = 264, kDEC = 270, kLE = 272, kTab = 276 };
+
+// Shared memory of a CTA.  Two buffers of each tile, the three terms of w C, and
+// X in one term; where X takes three, a has one buffer (it is free early: its two
+// products come first).
 template <int MODE>
 struct TcSmem {
-    static constexpr int NA = MODE == kOutDots ? 1 : 2, NB = 2, NC = MODE == kOutDots ? 1 : 2;
+    static constexpr int NA = MODE == kOutDots ? 1 : 2, NB = 2, NC = 2;
     static constexpr int XT = MODE == kOutDots ? 3 : 1;
     static constexpr uint32_t A = 0;
     static constexpr uint32_t B = A + (MODE == kStateOnly ? 0 : NA * 2 * kAtom);
@@ -54,21 +59,24 @@ struct TcSmem {
     static constexpr uint32_t CP = Cc + NC * kAtom;       // w C, three terms
     static constexpr uint32_t X = CP + 3 * kAtom;
     static constexpr uint32_t TAB = X + (MODE == kStateOnly ? 0 : XT * kAtom);
-    // tables of a chunk's decays (floats)
-    static constexpr int LC = 0, CF = 128, W = 256, EG = 384, RF = 512, DEC = 704;
-    static constexpr uint32_t BARS = TAB + 712 * 4;
-    static constexpr uint32_t TOTAL = BARS + 24 * 8 + 16;
+    static constexpr uint32_t BARS = TAB + 2 * kTab * 4;
+    static constexpr uint32_t TOTAL = BARS + 34 * 8 + 16;
+    static_assert(TOTAL <= 227 * 1024, "shared memory");
 };
 
-// Tensor memory columns.  SD: (w C)^T B, one column block per split term where
-// they fit, else the last two summed by the accumulator.
+// Tensor memory columns.  SD = (w C)^T B in two blocks, the first split term and
+// the other two: in one accumulator the small terms' steps round at the size of
+// the large one's sum (1.9e-7 of the state, against 6.5e-8 apart).  P is replaced
+// in place by its bf16 form (8 columns of each 16).  O = P C, OIN = A X^T: two
+// buffers each, so that a chunk's outputs are written after the next chunk's P,
+// whose products run meanwhile (LAG); with three terms of X, OIN has two blocks
+// and one buffer.
 template <int MODE>
 struct TcTmem {
-    static constexpr int SDW = MODE == kOutDots ? 128 : 192, INW = MODE == kOutDots ? 128 : 64;
-    static constexpr int SD = 0;
-    static constexpr int P = SDW, PB = P + 128, O = PB + 64, OIN = O + 64;
-    static constexpr uint32_t COLS = MODE == kStateOnly ? 256 : 512;
-    static_assert(MODE == kStateOnly || OIN + INW <= 512, "tensor memory");
+    static constexpr bool DOTS = MODE == kOutDots;
+    static constexpr int LAG = DOTS ? 0 : 1, NBUF = LAG + 1;
+    static constexpr int SD = 0, P = 128, O = 256, OIN = 384;
+    static constexpr uint32_t COLS = MODE == kStateOnly ? 128 : 512;
 };
 
 struct TcArgs {
@@ -78,7 +86,7 @@ struct TcArgs {
     float *gtot;         // state only: the blocks' sums of log-decays
     void *out;           // bf16, or fp32 with out32
     const __nv_bfloat16 *e;  // dots: rows that the state's part of out is multiplied with
-    float *dots;         // [column groups, rows, H]
+    float *dots;         // [2 x column groups, rows, H]
     int ha, hb, hc, he;  // heads of a, b, c, e
     int db, dc, ng;      // widths, column groups
     int tr;              // states are stored as the transpose of X
@@ -86,6 +94,15 @@ struct TcArgs {
     int out32, wide;     // out is fp32; out is 32-byte aligned
 };
 
+// Bounded wait: the loop rolled, for the kernels below are held back by the size
+// of their code.
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, unsigned int *err) {
+#pragma unroll 1
+    for (uint32_t i = 0; i < kSpinTc; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    if (err) atomicOr(err, kErrTimeout);
+    return false;
+}
 __device__ __forceinline__ void tma_load_3d(void *dst, const void *tmap, uint64_t *bar, int x, int y,
                                             int z) {
     asm volatile(
@@ -94,91 +111,193 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const void *tmap, uint64_
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
 }
+// MMAs and commits of one elected lane, in code that the whole warp runs: the
+// descriptors then live in uniform registers.  Under a branch on the lane each
+// MMA cost about ten instructions to move them there, which set its pace.
+__device__ __forceinline__ void mma_ss(uint32_t el, uint32_t d, uint64_t a, uint64_t b, uint32_t id,
+                                       uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(id), "r"(acc), "r"(el));
+}
+__device__ __forceinline__ void mma_ts(uint32_t el, uint32_t d, uint32_t a, uint64_t b, uint32_t id,
+                                       uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(id), "r"(acc), "r"(el));
+}
+__device__ __forceinline__ void commit(uint32_t el, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            smem_u32(bar)), "r"(el)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(e));
+    return e;
+}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float *v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+                 "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+                 "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
+                 "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
+                 : "memory");
 }
 __device__ __forceinline__ void st32(void *p, const uint32_t *w) {
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
                  "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
 }
+// Packed pairs of fp32 (one instruction for two).
+__device__ __forceinline__ uint64_t pk(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpk(uint64_t v, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ void mul2(float &a, float &b, float x, float y) {  // a *= x, b *= y
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pk(a, b)), "l"(pk(x, y)));
+    unpk(r, a, b);
+}
+__device__ __forceinline__ void add2(float &a, float &b, float x, float y) {  // a += x, b += y
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pk(a, b)), "l"(pk(x, y)));
+    unpk(r, a, b);
+}
+__device__ __forceinline__ void fma2(float &a, float &b, float m, float x, float y) {  // a += m x, b += m y
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pk(m, m)), "l"(pk(x, y)), "l"(pk(a, b)));
+    unpk(r, a, b);
+}
 // x0, x1 -> the bf16 pairs of the three truncated terms: x = hi + mid + lo, the
 // differences exact.
 __device__ __forceinline__ void split3(float x0, float x1, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
     const uint32_t u0 = __float_as_uint(x0), u1 = __float_as_uint(x1);
     hi = __byte_perm(u0, u1, 0x7632);
-    const float r0 = x0 - __uint_as_float(u0 & 0xffff0000u), r1 = x1 - __uint_as_float(u1 & 0xffff0000u);
+    float r0 = x0, r1 = x1;
+    add2(r0, r1, -__uint_as_float(u0 & 0xffff0000u), -__uint_as_float(u1 & 0xffff0000u));
     const uint32_t m0 = __float_as_uint(r0), m1 = __float_as_uint(r1);
     mid = __byte_perm(m0, m1, 0x7632);
-    const float l0 = r0 - __uint_as_float(m0 & 0xffff0000u), l1 = r1 - __uint_as_float(m1 & 0xffff0000u);
-    lo = __byte_perm(__float_as_uint(l0), __float_as_uint(l1), 0x7632);
+    add2(r0, r1, -__uint_as_float(m0 & 0xffff0000u), -__uint_as_float(m1 & 0xffff0000u));
+    lo = __byte_perm(__float_as_uint(r0), __float_as_uint(r1), 0x7632);
 }
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// The decays of one chunk (one warp; lane: 4 consecutive tokens), from 64-bit
-// running sums so that differences are rounded once.  The pair weights of a
-// 32 x 32 block off the diagonal are a product of a row factor and a column
-// factor around the border of the column's block, both at most 1 for decays:
-// no difference overflows; on the diagonal each is exponentiated (LC holds
-// the sums inside the block in units of log 2).
-template <bool REV, class SM>
-__device__ __forceinline__ void decay_tables(float *tab, const float (&gv)[4], int n, int lane) {
-    double p[4];
-    p[0] = gv[0];
-#pragma unroll
-    for (int u = 1; u < 4; ++u) p[u] = p[u - 1] + gv[u];
-    double inc = p[3];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-    }
-    const double base = inc - p[3], Gn = __shfl_sync(0xffffffffu, inc, 31);
-    double Gs[4];  // at the starts of the four 32-token blocks
-#pragma unroll
-    for (int b = 0; b < 4; ++b) Gs[b] = __shfl_sync(0xffffffffu, base, 8 * b);
-    const int kb = lane >> 3;
-    const double s0 = kb == 0 ? Gs[0] : kb == 1 ? Gs[1] : kb == 2 ? Gs[2] : Gs[3];
-    const double s1 = kb == 0 ? Gs[1] : kb == 1 ? Gs[2] : kb == 2 ? Gs[3] : Gn;
-    float lc[4], cf[4], w[4], eg[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const double G = base + p[u];
-        const bool in = 4 * lane + u < n;
-        lc[u] = (float)(G - s0) * kLog2e;
-        cf[u] = expf((float)(REV ? G - s0 : s1 - G));
-        w[u] = in ? expf((float)(REV ? G : Gn - G)) : 0.f;
-        eg[u] = expf((float)(REV ? Gn - G : G));
-    }
-    float4 *t4 = reinterpret_cast<float4 *>(tab);
-    t4[SM::LC / 4 + lane] = make_float4(lc[0], lc[1], lc[2], lc[3]);
-    t4[SM::CF / 4 + lane] = make_float4(cf[0], cf[1], cf[2], cf[3]);
-    t4[SM::W / 4 + lane] = make_float4(w[0], w[1], w[2], w[3]);
-    t4[SM::EG / 4 + lane] = make_float4(eg[0], eg[1], eg[2], eg[3]);
-    // row factors: forward, blocks before the row's own; reverse, blocks after it
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        if (REV ? b > kb : b < kb) {
-            float r[4];
-            const double e = REV ? Gs[b] : (b == 3 ? Gn : Gs[b + 1 < 4 ? b + 1 : 3]);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const double G = base + p[u];
-                r[u] = expf((float)(REV ? e - G : G - e));
-            }
-            // pair (row block kb, column block b) -> 32 entries at (pair index) * 32
-            const int hiB = REV ? b : kb, loB = REV ? kb : b;
-            t4[SM::RF / 4 + (hiB * (hiB - 1) / 2 + loB) * 8 + (lane & 7)] = make_float4(r[0], r[1], r[2], r[3]);
-        }
-    }
-    if (lane == 0) tab[SM::DEC] = expf((float)Gn);
+// A number in two floats, hi + lo (about 48 bits): sums by Knuth's exact two-sum.
+// The running sums of log-decays need it, for differences of far positions have to
+// be rounded once, not at the size of the sums.  In fp64 the sums took 6 times as
+// long: its units gave an addition every few hundred cycles beside the tensor
+// cores' work (forward, B4 T4096 H16 d128: 109 us, 90 so).
+struct Two {
+    float h, l;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {
+    const float s = a + b, t = s - a;
+    return {s, (a - (s - t)) + (b - t)};
+}
+__device__ __forceinline__ Two add(const Two &a, const Two &b) {
+    const Two s = two_sum(a.h, b.h);
+    const float l = s.l + (a.l + b.l), h = s.h + l;
+    return {h, l - (h - s.h)};
+}
+__device__ __forceinline__ float diff(const Two &a, const Two &b) {
+    const Two s = two_sum(a.h, -b.h);
+    return s.h + (s.l + (a.l - b.l));
+}
+__device__ __forceinline__ Two shfl(const Two &a, int lane) {
+    return {__shfl_sync(0xffffffffu, a.h, lane), __shfl_sync(0xffffffffu, a.l, lane)};
 }
 
+// The decays of one chunk (one warp; lane: 4 consecutive tokens), from running
+// sums G.  All weights are products of factors around the borders s_b, e_b of the
+// 32-token blocks, each at most 1 for decays, so nothing overflows:
+//   pair (i, j) in different blocks: row factor(i) BB(blocks) column factor(j),
+//     forward e^{G_i - s} and e^{e - G_j}, reverse e^{e - G_i} and e^{G_j - s};
+//   pair in one block: 2^(difference of LC);
+//   w_j = column factor(j) SE or SS(block), the state's weight = row factor(i) SS or SE,
+// SS_b = e^{s_b}, SE_b = e^{G_n - e_b}, BB = e^{s_later - e_earlier}.  Returns G_n.
+template <bool REV>
+__device__ __forceinline__ Two decay_tables(float *tab, const float (&gv)[4], int lane) {
+    Two p[4];
+    p[0] = {gv[0], 0.f};
+#pragma unroll
+    for (int u = 1; u < 4; ++u) p[u] = add(p[u - 1], {gv[u], 0.f});
+    Two inc = p[3];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const Two y = {__shfl_up_sync(0xffffffffu, inc.h, o), __shfl_up_sync(0xffffffffu, inc.l, o)};
+        const Two z = add(inc, y);
+        if (lane >= o) inc = z;
+    }
+    Two base = {__shfl_up_sync(0xffffffffu, inc.h, 1), __shfl_up_sync(0xffffffffu, inc.l, 1)};
+    if (lane == 0) base = {0.f, 0.f};
+    const Two Gn = shfl(inc, 31);
+    // the sum up to border b (0..4)
+    auto border = [&](int b) {
+        const Two y = shfl(base, 8 * (b & 3));
+        return b == 4 ? Gn : y;
+    };
+    const int kb = lane >> 3;
+    const Two s0 = border(kb), s1 = border(kb + 1);
+    float lc[4], cf[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const Two G = add(base, p[u]);
+        lc[u] = diff(G, s0) * kLog2e;
+        cf[u] = expf(REV ? diff(G, s0) : diff(s1, G));
+    }
+    reinterpret_cast<float4 *>(tab + kLC)[lane] = make_float4(lc[0], lc[1], lc[2], lc[3]);
+    reinterpret_cast<float4 *>(tab + kCF)[lane] = make_float4(cf[0], cf[1], cf[2], cf[3]);
+    // lanes 0-3 SS, 4-7 SE, 8-13 BB (pairs 10 20 21 30 31 32), 14 DEC, 16-19 LE
+    int hi = lane & 3, lo = 0;
+    if (lane >= 4 && lane < 8) { hi = 4; lo = lane - 3; }
+    if (lane >= 8 && lane < 14) {
+        hi = lane < 9 ? 1 : lane < 11 ? 2 : 3;
+        lo = lane - 8 - hi * (hi - 1) / 2 + 1;
+    }
+    if (lane == 14) hi = 4;
+    if (lane >= 16) { lo = lane & 3; hi = lo + 1; }
+    const Two bh = border(hi), bl = border(lo);
+    const float d = diff(bh, bl);
+    if (lane < 15 || (lane >= 16 && lane < 20)) tab[kSS + lane] = lane < 15 ? expf(d) : d * kLog2e;
+    return Gn;
+}
+// row factor of row i (block rb) from its LC
+template <bool REV>
+__device__ __forceinline__ float row_factor(const float *tab, int rb, float li) {
+    return exp2f(REV ? tab[kLE + rb] - li : li);
+}
+
+// Roles of the 21 warps: 8 of outputs, 8 of the state; TMA, decays, and the MMAs
+// of P, of A X^T and P C, and of (w C)^T B.  One thread gets an MMA through about
+// every 105 cycles whatever its width, so three issue.  Each role works a chunk
+// ahead of the one that needs its results, over mbarriers; no wait lags a barrier
+// by two phases (every phase needs an arrival of the waiter, or of one that
+// follows it).
+//
+// Loops over columns are rolled where they can be: the five roles' unrolled code
+// did not fit the instruction caches, and warps waited for instructions most of
+// the time (forward, B4 T4096 H16 d128: 225 us unrolled, 105 us rolled).
 template <bool REV, int MODE>
 __global__ void __launch_bounds__(kTcThreads, 1)
 chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
@@ -189,12 +308,14 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     extern __shared__ __align__(1024) uint8_t sm[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + SM::BARS);
     uint64_t *fullA = bars, *fullB = bars + 2, *fullC = bars + 4;      // tile loaded
-    uint64_t *freeA = bars + 6, *freeB = bars + 8, *freeC = bars + 10; // its products are done
-    uint64_t *pfull = bars + 12, *pfree = bars + 13, *pready = bars + 14, *ofull = bars + 15;
-    uint64_t *ifull = bars + 16, *ifree = bars + 17, *cready = bars + 18, *sfull = bars + 19;
-    uint64_t *xready = bars + 20, *tfull = bars + 21, *tfree = bars + 22;
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + 23);
-    float *tab = reinterpret_cast<float *>(sm + SM::TAB);
+    uint64_t *freeA = bars + 6, *freeB = bars + 8, *freeC = bars + 10; // its readers are done
+    uint64_t *pfull = bars + 12, *pready = bars + 14, *ofull = bars + 15;  // P and decays; its bf16 form; O
+    uint64_t *ifull = bars + 16, *ifree = bars + 18;                   // OIN; O and OIN written out
+    uint64_t *cready = bars + 20;                   // [2] w C, tokens 0-63 and 64-127
+    uint64_t *sfree = bars + 22, *sfull = bars + 23, *sdfree = bars + 24;  // first half done; SD
+    uint64_t *xready = bars + 25, *tfree = bars + 26, *zready = bars + 28;
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + 32);
+    float *tabs = reinterpret_cast<float *>(sm + SM::TAB);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     const int ng = blockIdx.x % p.ng, sh = blockIdx.x / p.ng;
@@ -220,28 +341,29 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         for (int i = 0; i < 2; ++i) {
             mbar_init(&fullA[i], 1);
             mbar_init(&fullB[i], 1);
-            mbar_init(&fullC[i], 1);
+            mbar_init(&fullC[i], 2);  // the tile and the chunk's decays
+            mbar_init(&pfull[i], 2);
+            mbar_init(&ifull[i], 1);
+            mbar_init(&ifree[i], 8);
             mbar_init(&freeA[i], 2);
             mbar_init(&freeB[i], MODE == kStateOnly ? 1 : 2);
-            mbar_init(&freeC[i], MODE == kStateOnly ? 1 : 5);  // O = P C; the 4 split warps
+            mbar_init(&freeC[i], MODE == kStateOnly ? 8 : 9);  // the 8 split warps; O = P C
+            mbar_init(&cready[i], 8);
+            mbar_init(&tfree[i], MODE == kStateOnly ? 8 : 16);
         }
-        mbar_init(pfull, 1);
-        mbar_init(pfree, 4);
-        mbar_init(pready, 4);
+        mbar_init(pready, 8);
         mbar_init(ofull, 1);
-        mbar_init(ifull, 1);
-        mbar_init(ifree, 4);
-        mbar_init(cready, 4);
+        mbar_init(sfree, 1);
         mbar_init(sfull, 1);
-        mbar_init(xready, 4);
-        mbar_init(tfull, 1);
-        mbar_init(tfree, MODE == kStateOnly ? 4 : 8);
+        mbar_init(sdfree, 8);
+        mbar_init(xready, 8);
+        mbar_init(zready, 8);
         fence_mbar_init();
         prefetch_tmap(&tm_b);
         prefetch_tmap(&tm_c);
         if (MODE != kStateOnly) prefetch_tmap(&tm_a);
     }
-    if (warp == 1) {
+    if (warp == 16) {
         tmem_alloc(tslot, TM::COLS);
         tmem_relinquish();
     }
@@ -251,282 +373,302 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     const uint32_t tmem = *tslot;
     const int na = p.db > 64 ? 2 : 1;  // 64-wide column blocks of a and b
     bool ok = true;
-    // chunk cc of the walk: first token and number of tokens
+    // first token of chunk cc of the walk
     auto chunk_at = [&](int cc) { return (REV ? nch - 1 - cc : cc) * kQ; };
 
-    if (warp == 0) {
-        // ===================== TMA loads =====================
-        if (lane == 0) {
-            for (int cc = 0; cc < nch && ok; ++cc) {
-                const int y = t0 + chunk_at(cc);
-                const int ib = cc % SM::NB, ic = cc % SM::NC, ia = cc % SM::NA;
-                if (cc >= SM::NB) ok = mbar_wait_bounded(&freeB[ib], (cc / SM::NB - 1) & 1, kSpinTc, err);
-                if (!ok) break;
-                mbar_arrive_expect_tx(&fullB[ib], na * kAtom);
-                for (int i = 0; i < na; ++i)
-                    tma_load_3d(sm + SM::B + (ib * 2 + i) * kAtom, &tm_b, &fullB[ib], 64 * i, hb, y);
-                if (MODE != kStateOnly) {
-                    if (cc >= SM::NA) ok = mbar_wait_bounded(&freeA[ia], (cc / SM::NA - 1) & 1, kSpinTc, err);
-                    if (!ok) break;
-                    mbar_arrive_expect_tx(&fullA[ia], na * kAtom);
-                    for (int i = 0; i < na; ++i)
-                        tma_load_3d(sm + SM::A + (ia * 2 + i) * kAtom, &tm_a, &fullA[ia], 64 * i, ha, y);
-                }
-                if (cc >= SM::NC) ok = mbar_wait_bounded(&freeC[ic], (cc / SM::NC - 1) & 1, kSpinTc, err);
-                if (!ok) break;
-                mbar_arrive_expect_tx(&fullC[ic], kAtom);
-                tma_load_3d(sm + SM::Cc + ic * kAtom, &tm_c, &fullC[ic], c0, hc, y);
-            }
-            // every load has landed and every product has read its tiles before the CTA ends:
-            // free(i) follows full(i), so waiting for the last use of each buffer covers both
-            for (int cc = nch - 1; cc >= 0 && cc >= nch - 2; --cc) {
-                if (cc >= nch - SM::NB) mbar_wait_bounded(&freeB[cc % SM::NB], (cc / SM::NB) & 1, kSpinTc, err);
-                if (MODE != kStateOnly && cc >= nch - SM::NA)
-                    mbar_wait_bounded(&freeA[cc % SM::NA], (cc / SM::NA) & 1, kSpinTc, err);
-                if (cc >= nch - SM::NC) mbar_wait_bounded(&freeC[cc % SM::NC], (cc / SM::NC) & 1, kSpinTc, err);
-            }
-        }
-    } else if (warp == 1) {
-        // ===================== MMA: P = A B^T, O = P C =====================
-        if (MODE != kStateOnly && lane == 0) {
-            const uint32_t idP = idesc_bf16(128, 128, 0, 0), idO = idesc_bf16(128, kN, 0, 1);
-            const uint64_t dA = sdesc_sw128(smem_u32(sm + SM::A), 16, 1024);
-            const uint64_t dB = sdesc_sw128(smem_u32(sm + SM::B), 16, 1024);
-            const uint64_t dC = sdesc_sw128(smem_u32(sm + SM::Cc), kAtom, 1024);
-            const int ks = p.db / 16;
-            auto gram = [&](int cc) {
-                const int ia = cc % SM::NA, ib = cc % SM::NB;
-                ok = ok && mbar_wait_bounded(&fullA[ia], (cc / SM::NA) & 1, kSpinTc, err);
-                ok = ok && mbar_wait_bounded(&fullB[ib], (cc / SM::NB) & 1, kSpinTc, err);
-                // rows past the end are zeroed before they are multiplied (the short chunk is the
-                // first or the last of the walk, so cready cannot be two phases ahead of this wait)
-                if (len - chunk_at(cc) < kQ) ok = ok && mbar_wait_bounded(cready, cc & 1, kSpinTc, err);
-                if (cc > 0) ok = ok && mbar_wait_bounded(pfree, (cc - 1) & 1, kSpinTc, err);
-                if (!ok) return;
-                tc_fence_after();
-                for (int kk = 0; kk < ks; ++kk) {
-                    const uint32_t o = (kk >> 2) * kAtom + (kk & 3) * 32;
-                    mma_bf16_ss(tmem + TM::P, sdesc_add(dA, ia * 2 * kAtom + o),
-                                sdesc_add(dB, ib * 2 * kAtom + o), idP, kk > 0);
-                }
-                mma_commit(&freeA[ia]);
-                mma_commit(&freeB[ib]);
-                mma_commit(pfull);
-            };
-            if (nch > 0) gram(0);
-            for (int cc = 0; cc < nch && ok; ++cc) {
-                const int ic = cc % SM::NC;
-                ok = ok && mbar_wait_bounded(&fullC[ic], (cc / SM::NC) & 1, kSpinTc, err);
-                ok = ok && mbar_wait_bounded(pready, cc & 1, kSpinTc, err);
-                if (!ok) break;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_bf16_ts(tmem + TM::O, tmem + TM::PB + kk * 8,
-                                sdesc_add(dC, ic * kAtom + kk * 2048), idO, kk > 0);
-                mma_commit(&freeC[ic]);
-                mma_commit(ofull);
-                if (cc + 1 < nch) gram(cc + 1);
-            }
-        }
-    } else if (warp == 2) {
-        // ===================== MMA: A X^T, (w C)^T B =====================
-        if (lane == 0) {
-            const uint64_t dA = sdesc_sw128(smem_u32(sm + SM::A), 16, 1024);
-            const uint64_t dX = sdesc_sw128(smem_u32(sm + SM::X), kAtom, 1024);
-            // b as [d_b, tokens]: with one 64-wide block the upper lanes repeat it (not read)
-            const uint64_t dB = sdesc_sw128(smem_u32(sm + SM::B), na > 1 ? kAtom : 0, 1024);
-            const uint64_t dP = sdesc_sw128(smem_u32(sm + SM::CP), kAtom, 1024);
-            const int ks = p.db / 16;
-            for (int cc = 0; cc < nch && ok; ++cc) {
-                const int ia = cc % SM::NA, ib = cc % SM::NB;
-                if (MODE != kStateOnly) {
-                    ok = ok && mbar_wait_bounded(&fullA[ia], (cc / SM::NA) & 1, kSpinTc, err);
-                    ok = ok && mbar_wait_bounded(xready, cc & 1, kSpinTc, err);
-                    if (cc > 0) ok = ok && mbar_wait_bounded(ifree, (cc - 1) & 1, kSpinTc, err);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t idI = idesc_bf16(128, TM::INW, 0, 1), idL = idesc_bf16(128, kN, 0, 1);
-                    for (int kk = 0; kk < ks; ++kk)
-                        mma_bf16_ss(tmem + TM::OIN,
-                                    sdesc_add(dA, ia * 2 * kAtom + (kk >> 2) * kAtom + (kk & 3) * 32),
-                                    sdesc_add(dX, kk * 2048), idI, kk > 0);
-                    if (MODE == kOutDots)
-                        for (int kk = 0; kk < ks; ++kk)
-                            mma_bf16_ss(tmem + TM::OIN + kN,
-                                        sdesc_add(dA, ia * 2 * kAtom + (kk >> 2) * kAtom + (kk & 3) * 32),
-                                        sdesc_add(dX, 2 * kAtom + kk * 2048), idL, 1);
-                    mma_commit(&freeA[ia]);
-                    mma_commit(ifull);
-                }
-                ok = ok && mbar_wait_bounded(&fullB[ib], (cc / SM::NB) & 1, kSpinTc, err);
-                ok = ok && mbar_wait_bounded(cready, cc & 1, kSpinTc, err);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t idS = idesc_bf16(128, TM::SDW, 1, 1), idT = idesc_bf16(128, kN, 1, 1);
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_bf16_ss(tmem + TM::SD, sdesc_add(dB, ib * 2 * kAtom + kk * 2048),
-                                sdesc_add(dP, kk * 2048), idS, kk > 0);
-                if (TM::SDW == 128)
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        mma_bf16_ss(tmem + TM::SD + kN, sdesc_add(dB, ib * 2 * kAtom + kk * 2048),
-                                    sdesc_add(dP, 2 * kAtom + kk * 2048), idT, 1);
-                if (MODE == kStateOnly) mma_commit(&freeC[cc % SM::NC]);
-                mma_commit(&freeB[ib]);
-                mma_commit(sfull);
-            }
-        }
-    } else if (warp == 3) {
-        // ===================== decays =====================
-        float gv[4], gt = 0.f;
+    if (warp == 16) {
+        // ===================== TMA loads and decays =====================
+        float gv[4];
         auto load = [&](int cc) {
             const int j0 = chunk_at(cc), n = min(kQ, len - j0);
 #pragma unroll
             for (int u = 0; u < 4; ++u)
                 gv[u] = 4 * lane + u < n ? load_g(geo, p.g, (long)t0 + j0 + 4 * lane + u, h) : 0.f;
         };
-        double tot = 0.0;
-        if (nch > 0) load(0);
-        for (int cc = 0; cc < nch && ok; ++cc) {
-            const int n = min(kQ, len - chunk_at(cc));
-            if (cc > 0) ok = mbar_wait_bounded(tfree, (cc - 1) & 1, kSpinTc, err);
+        Two tot = {0.f, 0.f};
+        // the tiles of chunk cc, as their buffers fall free.  (The whole warp waits: with the waits
+        // under a branch on the lane, the code after it ran apart for that lane, and the decays
+        // took five times as long.)
+        auto issue = [&](int cc) {
+            const int i2 = cc & 1, y = t0 + chunk_at(cc), ia = SM::NA == 2 ? i2 : 0;
+            if (cc >= 2) ok = ok && wait(&freeB[i2], (cc / 2 - 1) & 1, err);
+            if (ok && lane == 0) {
+                mbar_arrive_expect_tx(&fullB[i2], na * kAtom);
+                for (int i = 0; i < na; ++i)
+                    tma_load_3d(sm + SM::B + (i2 * 2 + i) * kAtom, &tm_b, &fullB[i2], 64 * i, hb, y);
+            }
+            __syncwarp();
+            if (MODE != kStateOnly) {
+                if (cc >= SM::NA) ok = ok && wait(&freeA[ia], (cc / SM::NA - 1) & 1, err);
+                if (ok && lane == 0) {
+                    mbar_arrive_expect_tx(&fullA[ia], na * kAtom);
+                    for (int i = 0; i < na; ++i)
+                        tma_load_3d(sm + SM::A + (ia * 2 + i) * kAtom, &tm_a, &fullA[ia], 64 * i, ha, y);
+                }
+                __syncwarp();
+            }
+            if (cc >= 2) ok = ok && wait(&freeC[i2], (cc / 2 - 1) & 1, err);
+            if (ok && lane == 0) {
+                mbar_arrive_expect_tx(&fullC[i2], kAtom);
+                tma_load_3d(sm + SM::Cc + i2 * kAtom, &tm_c, &fullC[i2], c0, hc, y);
+            }
+            __syncwarp();
+        };
+        if (nch > 0) {
+            load(0);
+            issue(0);
+        }
+        for (int cc = 0; cc < nch; ++cc) {
+            // the decays of chunk cc before its tiles: their buffer is free earlier
+            const int i2 = cc & 1;
+            if (cc >= 2) ok = ok && wait(&tfree[i2], (cc / 2 - 1) & 1, err);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            decay_tables<REV, SM>(tab, gv, n, lane);
-            if (MODE == kStateOnly) tot += (double)gv[0] + gv[1] + gv[2] + gv[3];
+            tot = add(tot, decay_tables<REV>(tabs + i2 * kTab, gv, lane));
             __syncwarp();
-            if (lane == 0) mbar_arrive(tfull);
+            if (lane == 0) {
+                mbar_arrive(&fullC[i2]);
+                if (MODE != kStateOnly) mbar_arrive(&pfull[i2]);
+            }
+            __syncwarp();
             if (cc + 1 < nch) load(cc + 1);
+            if (cc > 0) issue(cc);
         }
         if (MODE == kStateOnly && p.gtot && ng == 0) {
+            if (lane == 0) p.gtot[(size_t)slot * geo.H + h] = tot.h;
+        }
+        // every load has landed and every product has read its tiles before the CTA ends:
+        // free(i) follows full(i), so waiting for the last use of each buffer covers both
+        for (int cc = max(nch - 2, 0); cc < nch; ++cc) {
+            wait(&freeB[cc & 1], (cc / 2) & 1, err);
+            wait(&freeC[cc & 1], (cc / 2) & 1, err);
+            if (MODE != kStateOnly && cc >= nch - SM::NA)
+                wait(&freeA[SM::NA == 2 ? cc & 1 : 0], (cc / SM::NA) & 1, err);
+        }
+        __syncwarp();
+    } else if (warp == 17) {
+        // ===================== MMA: P = A B^T =====================
+        if (MODE != kStateOnly) {
+            const uint32_t el = elect_lane(), idP = idesc_bf16(128, 128, 0, 0);
+            const uint64_t dA = sdesc_sw128(smem_u32(sm + SM::A), 16, 1024);
+            const uint64_t dB = sdesc_sw128(smem_u32(sm + SM::B), 16, 1024);
+            const int ks = p.db / 16;
+            for (int cc = 0; cc < nch; ++cc) {
+                const int i2 = cc & 1, ia = SM::NA == 2 ? i2 : 0;
+                ok = ok && wait(&fullA[ia], (cc / SM::NA) & 1, err);
+                ok = ok && wait(&fullB[i2], (cc >> 1) & 1, err);
+                // rows past the end are zeroed before they are multiplied (one chunk of the walk)
+                if (len - chunk_at(cc) < kQ) ok = ok && wait(zready, 0, err);
+                if (cc > 0) ok = ok && wait(ofull, (cc - 1) & 1, err);  // the last P is read
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t da = sdesc_add(dA, ia * 2 * kAtom), db = sdesc_add(dB, i2 * 2 * kAtom);
 #pragma unroll
-            for (int o = 16; o; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
-            gt = (float)tot;
-            if (lane == 0) p.gtot[(size_t)slot * geo.H + h] = gt;
+                for (int kk = 0; kk < 8; ++kk)
+                    if (kk < ks) {
+                        const uint32_t o = (kk >> 2) * kAtom + (kk & 3) * 32;
+                        mma_ss(el, tmem + TM::P, sdesc_add(da, o), sdesc_add(db, o), idP, kk > 0);
+                    }
+                commit(el, &freeA[ia]);
+                commit(el, &freeB[i2]);
+                commit(el, &pfull[i2]);
+            }
+        }
+    } else if (warp == 18) {
+        // ===================== MMA: OIN = A X^T, O = P C =====================
+        if (MODE != kStateOnly) {
+            const uint32_t el = elect_lane(), idN = idesc_bf16(128, kN, 0, 1);
+            const uint64_t dA = sdesc_sw128(smem_u32(sm + SM::A), 16, 1024);
+            const uint64_t dC = sdesc_sw128(smem_u32(sm + SM::Cc), kAtom, 1024);
+            const uint64_t dX = sdesc_sw128(smem_u32(sm + SM::X), kAtom, 1024);
+            const int ks = p.db / 16;
+            for (int cc = 0; cc < nch; ++cc) {
+                const int i2 = cc & 1, ia = SM::NA == 2 ? i2 : 0;
+                ok = ok && wait(&fullA[ia], (cc / SM::NA) & 1, err);
+                ok = ok && wait(xready, cc & 1, err);
+                if (cc >= TM::NBUF) ok = ok && wait(&ifree[cc % TM::NBUF], (cc / TM::NBUF - 1) & 1, err);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t da = sdesc_add(dA, ia * 2 * kAtom);
+                const uint32_t tI = tmem + TM::OIN + cc % TM::NBUF * kN, tO = tmem + TM::O + cc % TM::NBUF * kN;
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    if (kk < ks) {
+                        const uint64_t a = sdesc_add(da, (kk >> 2) * kAtom + (kk & 3) * 32);
+                        const uint64_t b = sdesc_add(dX, kk * 2048);
+                        mma_ss(el, tI, a, b, idN, kk > 0);
+                        if (TM::DOTS) {
+                            mma_ss(el, tI + kN, a, sdesc_add(b, kAtom), idN, kk > 0);
+                            mma_ss(el, tI + kN, a, sdesc_add(b, 2 * kAtom), idN, 1);
+                        }
+                    }
+                commit(el, &freeA[ia]);
+                commit(el, &ifull[cc % TM::NBUF]);
+                ok = ok && wait(&fullC[i2], (cc >> 1) & 1, err);
+                ok = ok && wait(pready, cc & 1, err);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t d = sdesc_add(dC, i2 * kAtom);
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    mma_ts(el, tO, tmem + TM::P + kk * 16, sdesc_add(d, kk * 2048), idN, kk > 0);
+                commit(el, &freeC[i2]);
+                commit(el, ofull);
+            }
+        }
+    } else if (warp == 19) {
+        // ===================== MMA: SD = (w C)^T B, half the tokens at a time =====================
+        {
+            const uint32_t el = elect_lane(), idS = idesc_bf16(128, kN, 1, 1);
+            // b as [d_b, tokens]: with one 64-wide block the upper lanes repeat it (not read)
+            const uint64_t dB = sdesc_sw128(smem_u32(sm + SM::B), na > 1 ? kAtom : 0, 1024);
+            const uint64_t dP = sdesc_sw128(smem_u32(sm + SM::CP), kAtom, 1024);
+            for (int cc = 0; cc < nch; ++cc) {
+                const int i2 = cc & 1;
+                ok = ok && wait(&fullB[i2], (cc >> 1) & 1, err);
+                if (cc > 0) ok = ok && wait(sdfree, (cc - 1) & 1, err);
+                const uint64_t db = sdesc_add(dB, i2 * 2 * kAtom);
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    ok = ok && wait(&cready[hf], cc & 1, err);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 4 * hf; kk < 4 * hf + 4; ++kk) {
+                        const uint64_t a = sdesc_add(db, kk * 2048), b = sdesc_add(dP, kk * 2048);
+                        mma_ss(el, tmem + TM::SD, a, b, idS, kk > 0);
+                        mma_ss(el, tmem + TM::SD + kN, a, sdesc_add(b, kAtom), idS, kk > 0);
+                        mma_ss(el, tmem + TM::SD + kN, a, sdesc_add(b, 2 * kAtom), idS, 1);
+                    }
+                    if (hf == 0) commit(el, sfree);
+                }
+                if (!ok) break;
+                commit(el, &freeB[i2]);
+                commit(el, sfull);
+            }
         }
     } else if (warp < 8) {
-        // ===================== outputs: row i of the chunk =====================
+        // ===================== outputs: row i of the chunk, half the columns =====================
+        // P of chunk cc, then the outputs of chunk cc - LAG
         if (MODE != kStateOnly) {
-            const int rb = warp & 3, i = rb * 32 + lane;
+            const int rb = warp & 3, hf = warp >> 2, i = rb * 32 + lane;
             const uint32_t lb = (uint32_t)(rb * 32) << 16;
-            for (int cc = 0; cc < nch; ++cc) {
-                const int j0 = chunk_at(cc), n = min(kQ, len - j0);
-                ok = ok && mbar_wait_bounded(tfull, cc & 1, kSpinTc, err);
-                ok = ok && mbar_wait_bounded(pfull, cc & 1, kSpinTc, err);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                tc_fence_after();
-                const float eg = tab[SM::EG + i], li = tab[SM::LC + i];
-                // weights of the pairs, 32 columns at a time
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    float w[32];
-                    if (REV ? b < rb : b > rb) {
-#pragma unroll
-                        for (int u = 0; u < 16; ++u) w[u] = 0.f;
-                    } else {
-                        float x[32];
-                        tmem_ld16(tmem + TM::P + lb + 32 * b, x);
-                        tmem_ld16(tmem + TM::P + lb + 32 * b + 16, x + 16);
-                        tmem_wait_ld();
-                        if (b == rb) {
-#pragma unroll
-                            for (int u = 0; u < 32; ++u) {
-                                const float lj = tab[SM::LC + 32 * b + u];
-                                const bool in = REV ? u >= lane : u <= lane;
-                                x[u] = in ? x[u] * ex2(REV ? lj - li : li - lj) : 0.f;
-                            }
-                        } else {
-                            const int hiB = REV ? b : rb, loB = REV ? rb : b;
-                            const float r = tab[SM::RF + (hiB * (hiB - 1) / 2 + loB) * 32 + lane];
-#pragma unroll
-                            for (int u4 = 0; u4 < 8; ++u4) {
-                                const float4 c = *reinterpret_cast<const float4 *>(tab + SM::CF + 32 * b + 4 * u4);
-                                x[4 * u4] *= r * c.x;
-                                x[4 * u4 + 1] *= r * c.y;
-                                x[4 * u4 + 2] *= r * c.z;
-                                x[4 * u4 + 3] *= r * c.w;
-                            }
-                        }
-#pragma unroll
-                        for (int u = 0; u < 16; ++u) w[u] = __uint_as_float(pack2(x[2 * u], x[2 * u + 1]));
-                    }
-                    tmem_st16(tmem + TM::PB + lb + 16 * b, w);
-                }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(pready);
-                    mbar_arrive(pfree);
-                    mbar_arrive(tfree);
-                }
-                const size_t row = (size_t)t0 + j0 + i;
-                ok = ok && mbar_wait_bounded(ifull, cc & 1, kSpinTc, err);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                tc_fence_after();
-                float o[64];
-#pragma unroll
-                for (int b = 0; b < 4; ++b) tmem_ld16(tmem + TM::OIN + lb + 16 * b, o + 16 * b);
-                if (MODE == kOutDots) {
-                    float m[64];
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) tmem_ld16(tmem + TM::OIN + kN + lb + 16 * b, m + 16 * b);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int u = 0; u < 64; ++u) o[u] = eg * (o[u] + m[u]);
-                } else {
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int u = 0; u < 64; ++u) o[u] *= eg;
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(ifree);
-                if (MODE == kOutDots && i < n) {
-                    float d = 0.f;
-                    const __nv_bfloat16 *e = p.e + (row * p.he + h / (geo.H / p.he)) * p.dc + c0;
-#pragma unroll
-                    for (int b = 0; b < 8; ++b)
-                        if (c0 + 8 * b < p.dc) {
-                            float f[8];
-                            unpack8(*reinterpret_cast<const uint4 *>(e + 8 * b), f);
-#pragma unroll
-                            for (int u = 0; u < 8; ++u) d = fmaf(o[8 * b + u], f[u], d);
-                        }
-                    p.dots[((size_t)ng * geo.rows + row) * geo.H + h] = d;
-                }
-                ok = ok && mbar_wait_bounded(ofull, cc & 1, kSpinTc, err);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                tc_fence_after();
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    float x[16];
-                    tmem_ld16(tmem + TM::O + lb + 16 * b, x);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int u = 0; u < 16; ++u) o[16 * b + u] += x[u];
-                }
-                tc_fence_before();
-                if (i < n) {
-                    const size_t at = (row * geo.H + h) * p.dc + c0;
-#pragma unroll
+            const int ncb = min(kN, p.dc - c0) >> 4;
+            float eg = 0.f;  // weight of the state that entered chunk cc - 1
+            for (int cc = 0; cc < nch + TM::LAG; ++cc) {
+                float egn = 0.f;
+                if (cc < nch) {
+                    const float *tab = tabs + (cc & 1) * kTab;
+                    ok = ok && wait(&pfull[cc & 1], (cc >> 1) & 1, err);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const float li = tab[kLC + i], rf = row_factor<REV>(tab, rb, li);
+                    egn = rf * tab[(REV ? kSE : kSS) + rb];
+                    // weights of the pairs: this half's 16 columns of each block
+#pragma unroll 1
                     for (int b = 0; b < 4; ++b) {
-                        if (c0 + 16 * b >= p.dc) continue;
-                        if (p.out32) {
+                        const int col = 32 * b + 16 * hf;
+                        float w[8];
+                        if (REV ? b < rb : b > rb) {
+#pragma unroll
+                            for (int u = 0; u < 8; ++u) w[u] = 0.f;
+                        } else {
+                            float x[16], f[16];
+                            tmem_ld16(tmem + TM::P + lb + col, x);
+#pragma unroll
+                            for (int u4 = 0; u4 < 4; ++u4) {
+                                const float4 l = *reinterpret_cast<const float4 *>(
+                                    tab + (b == rb ? kLC : kCF) + col + 4 * u4);
+                                f[4 * u4] = l.x; f[4 * u4 + 1] = l.y; f[4 * u4 + 2] = l.z; f[4 * u4 + 3] = l.w;
+                            }
+                            if (b == rb) {
+#pragma unroll
+                                for (int u = 0; u < 16; ++u) f[u] = ex2(REV ? f[u] - li : li - f[u]);
+                            } else {
+                                const int hiB = REV ? b : rb, loB = REV ? rb : b;
+                                const float r = rf * tab[kBB + hiB * (hiB - 1) / 2 + loB];
+#pragma unroll
+                                for (int u = 0; u < 16; u += 2) mul2(f[u], f[u + 1], r, r);
+                            }
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int u = 0; u < 16; u += 2) mul2(x[u], x[u + 1], f[u], f[u + 1]);
+                            if (b == rb) {  // a select, so that what lies outside cannot matter
+#pragma unroll
+                                for (int u = 0; u < 16; ++u) {
+                                    const bool in = REV ? u + 16 * hf >= lane : u + 16 * hf <= lane;
+                                    x[u] = in ? x[u] : 0.f;
+                                }
+                            }
+#pragma unroll
+                            for (int u = 0; u < 8; ++u) w[u] = __uint_as_float(pack2(x[2 * u], x[2 * u + 1]));
+                        }
+                        tmem_st8(tmem + TM::P + lb + col, w);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(pready);
+                        mbar_arrive(&tfree[cc & 1]);
+                    }
+                }
+                if (cc >= TM::LAG) {
+                    const int pc = cc - TM::LAG, ib = pc % TM::NBUF, j0 = chunk_at(pc), n = min(kQ, len - j0);
+                    const size_t row = (size_t)t0 + j0 + i;
+                    ok = ok && wait(&ifull[ib], (pc / TM::NBUF) & 1, err);
+                    // (with LAG, P of chunk cc was formed after this product)
+                    if (!TM::LAG || cc == nch) ok = ok && wait(ofull, pc & 1, err);
+                    if (!TM::LAG) eg = egn;
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    float d = 0.f;
+                    const __nv_bfloat16 *e = nullptr;
+                    if (MODE == kOutDots) e = p.e + (row * p.he + h / (geo.H / p.he)) * p.dc + c0;
+                    const size_t at = (row * geo.H + h) * p.dc + c0;
+#pragma unroll 1
+                    for (int b = 2 * hf; b < min(ncb, 2 * hf + 2); ++b) {
+                        float o[16], y[16];
+                        tmem_ld16(tmem + TM::OIN + ib * kN + lb + 16 * b, o);
+                        tmem_ld16(tmem + TM::O + ib * kN + lb + 16 * b, y);
+                        if (MODE == kOutDots) {
+                            float m[16];
+                            tmem_ld16(tmem + TM::OIN + kN + lb + 16 * b, m);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int u = 0; u < 16; u += 2) {
+                                add2(o[u], o[u + 1], m[u], m[u + 1]);
+                                mul2(o[u], o[u + 1], eg, eg);
+                            }
+                            if (i < n) {
+                                float f[16];
+                                unpack8(*reinterpret_cast<const uint4 *>(e + 16 * b), f);
+                                unpack8(*reinterpret_cast<const uint4 *>(e + 16 * b + 8), f + 8);
+#pragma unroll
+                                for (int u = 0; u < 16; ++u) d = fmaf(o[u], f[u], d);
+                            }
+#pragma unroll
+                            for (int u = 0; u < 16; u += 2) add2(y[u], y[u + 1], o[u], o[u + 1]);
+                        } else {
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int u = 0; u < 16; u += 2) fma2(y[u], y[u + 1], eg, o[u], o[u + 1]);
+                        }
+                        if (i < n && p.out32) {
                             float4 *q = reinterpret_cast<float4 *>((float *)p.out + at + 16 * b);
 #pragma unroll
                             for (int u = 0; u < 4; ++u)
-                                q[u] = make_float4(o[16 * b + 4 * u], o[16 * b + 4 * u + 1],
-                                                   o[16 * b + 4 * u + 2], o[16 * b + 4 * u + 3]);
-                        } else {
+                                q[u] = make_float4(y[4 * u], y[4 * u + 1], y[4 * u + 2], y[4 * u + 3]);
+                        } else if (i < n) {
                             uint32_t w[8];
 #pragma unroll
-                            for (int u = 0; u < 8; ++u) w[u] = pack2(o[16 * b + 2 * u], o[16 * b + 2 * u + 1]);
+                            for (int u = 0; u < 8; ++u) w[u] = pack2(y[2 * u], y[2 * u + 1]);
                             __nv_bfloat16 *q = (__nv_bfloat16 *)p.out + at + 16 * b;
                             if (p.wide) {
                                 st32(q, w);
@@ -535,37 +677,134 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                                 reinterpret_cast<uint4 *>(q)[1] = make_uint4(w[4], w[5], w[6], w[7]);
                             }
                         }
+                        __syncwarp();  // the loads above are warp-wide
                     }
+                    if (MODE == kOutDots && i < n)
+                        p.dots[((size_t)(2 * ng + hf) * geo.rows + row) * geo.H + h] = d;
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ifree[ib]);
                 }
+                eg = egn;
             }
         }
     } else {
-        // ===================== state: row k of X^T (d_b), 64 columns =====================
-        const int rb = warp & 3, k = rb * 32 + lane;
+        // ===================== state: row k of X^T (d_b), half of the 64 columns =====================
+        const int rb = warp & 3, hf = (warp >> 2) - 2, k = rb * 32 + lane;
+        const int cx = c0 + 32 * hf;  // first column
         const uint32_t lb = (uint32_t)(rb * 32) << 16;
-        float x[64];
+        float x[32];
 #pragma unroll
-        for (int u = 0; u < 64; ++u) x[u] = 0.f;
+        for (int u = 0; u < 32; ++u) x[u] = 0.f;
         const size_t unit = (size_t)(p.multi ? slot : sl.z) * geo.H + h;
         if (MODE != kStateOnly && p.xin && k < p.db) {
             const float *src = p.xin + unit * nel;
             if (p.tr) {
 #pragma unroll
-                for (int u = 0; u < 16; ++u)
-                    if (c0 + 4 * u < p.dc) {
-                        const float4 y = *reinterpret_cast<const float4 *>(src + (size_t)k * p.dc + c0 + 4 * u);
+                for (int u = 0; u < 8; ++u)
+                    if (cx + 4 * u < p.dc) {
+                        const float4 y = *reinterpret_cast<const float4 *>(src + (size_t)k * p.dc + cx + 4 * u);
                         x[4 * u] = y.x; x[4 * u + 1] = y.y; x[4 * u + 2] = y.z; x[4 * u + 3] = y.w;
                     }
             } else {
 #pragma unroll
-                for (int u = 0; u < 64; ++u)
-                    if (c0 + u < p.dc) x[u] = src[(size_t)(c0 + u) * p.db + k];
+                for (int u = 0; u < 32; ++u)
+                    if (cx + u < p.dc) x[u] = src[(size_t)(cx + u) * p.db + k];
             }
         }
-        auto publish = [&]() {  // X as the B operand of A X^T: row k, swizzled
+        // split of w C: row sr of a half's 64 tokens, 16 columns
+        const int sw = warp - 8, sr = (sw & 1) * 32 + lane, sq = (sw >> 1) * 2;
+        float dec = 0.f;  // decay over chunk cc - 1
+        for (int cc = 0; cc <= nch; ++cc) {
+            const int i2 = cc & 1, n = cc < nch ? min(kQ, len - chunk_at(cc)) : 0;
+            const float *tab = tabs + i2 * kTab;
+            float decn = 0.f;
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                if (cc < nch) {
+                    if (half == 0) {
+                        ok = ok && wait(&fullC[i2], (cc >> 1) & 1, err);
+                        if (n < kQ) ok = ok && wait(&fullB[i2], (cc >> 1) & 1, err);
+                        if (cc > 0) ok = ok && wait(sfree, (cc - 1) & 1, err);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                    }
+                    const int j = 64 * half + sr;
+                    const float w = tab[kCF + j] * tab[(REV ? kSS : kSE) + (j >> 5)];
+                    uint8_t *crow = sm + SM::Cc + i2 * kAtom + j * 128;
+                    uint8_t *prow = sm + SM::CP + j * 128;
+#pragma unroll 1
+                    for (int b = sq; b < sq + 2; ++b) {
+                        const int off = (b ^ (j & 7)) << 4;
+                        uint4 hi, mid, lo;
+                        hi = mid = lo = make_uint4(0, 0, 0, 0);
+                        if (j < n) {
+                            float f[8];
+                            unpack8(*reinterpret_cast<const uint4 *>(crow + off), f);
 #pragma unroll
-            for (int b = 0; b < 8; ++b) {
-                const uint32_t off = SM::X + k * 128 + ((b ^ (k & 7)) << 4);
+                            for (int u = 0; u < 8; u += 2) mul2(f[u], f[u + 1], w, w);
+                            split3(f[0], f[1], hi.x, mid.x, lo.x);
+                            split3(f[2], f[3], hi.y, mid.y, lo.y);
+                            split3(f[4], f[5], hi.z, mid.z, lo.z);
+                            split3(f[6], f[7], hi.w, mid.w, lo.w);
+                        } else {  // past the end: zero, whatever memory holds there
+                            *reinterpret_cast<uint4 *>(crow + off) = hi;
+                            for (int t = 0; t < na; ++t)
+                                *reinterpret_cast<uint4 *>(sm + SM::B + (i2 * 2 + t) * kAtom + j * 128 + off) = hi;
+                        }
+                        *reinterpret_cast<uint4 *>(prow + off) = hi;
+                        *reinterpret_cast<uint4 *>(prow + off + kAtom) = mid;
+                        *reinterpret_cast<uint4 *>(prow + off + 2 * kAtom) = lo;
+                    }
+                    decn = tab[kDEC];
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&cready[half]);
+                        if (half == 1) {
+                            mbar_arrive(&freeC[i2]);
+                            mbar_arrive(&tfree[i2]);
+                            if (n < kQ) mbar_arrive(zready);
+                        }
+                    }
+                }
+                if (half == 0 && cc > 0) {  // X <- e^{G_n} X + SD of chunk cc - 1
+                    ok = ok && wait(sfull, (cc - 1) & 1, err);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const uint32_t col = tmem + TM::SD + lb + 32 * hf + 8 * b;
+                        float hi[8], mid[8];
+                        tmem_ld8(col, hi);
+                        tmem_ld8(col + kN, mid);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int u = 0; u < 8; u += 2) {
+                            add2(hi[u], hi[u + 1], mid[u], mid[u + 1]);
+                            fma2(hi[u], hi[u + 1], dec, x[8 * b + u], x[8 * b + u + 1]);
+                            x[8 * b + u] = hi[u];
+                            x[8 * b + u + 1] = hi[u + 1];
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sdfree);
+                }
+            }
+            if (!ok) break;
+            dec = decn;
+            if (MODE == kStateOnly || cc == nch) continue;
+            // X as the B operand of A X^T (row k, swizzled), once the last chunk's product is done
+            if (cc > 0) {
+                ok = ok && wait(&ifull[(cc - 1) % TM::NBUF], ((cc - 1) / TM::NBUF) & 1, err);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+            }
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const uint32_t off = SM::X + k * 128 + (((4 * hf + b) ^ (k & 7)) << 4);
                 if (MODE == kOutDots) {
                     uint4 hi, mid, lo;
                     split3(x[8 * b], x[8 * b + 1], hi.x, mid.x, lo.x);
@@ -582,96 +821,26 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(xready);
-        };
-        if (MODE != kStateOnly) publish();
-        for (int cc = 0; cc < nch; ++cc) {
-            const int n = min(kQ, len - chunk_at(cc)), ib = cc % SM::NB, ic = cc % SM::NC;
-            ok = ok && mbar_wait_bounded(tfull, cc & 1, kSpinTc, err);
-            ok = ok && mbar_wait_bounded(&fullC[ic], (cc / SM::NC) & 1, kSpinTc, err);
-            if (n < kQ) ok = ok && mbar_wait_bounded(&fullB[ib], (cc / SM::NB) & 1, kSpinTc, err);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            const float w = tab[SM::W + k], dec = tab[SM::DEC];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(tfree);
-            uint8_t *crow = sm + SM::Cc + ic * kAtom + k * 128;
-            uint8_t *prow = sm + SM::CP + k * 128;
-            if (k < n) {
-#pragma unroll
-                for (int b = 0; b < 8; ++b) {
-                    float f[8];
-                    unpack8(*reinterpret_cast<const uint4 *>(crow + ((b ^ (k & 7)) << 4)), f);
-                    uint4 hi, mid, lo;
-                    split3(w * f[0], w * f[1], hi.x, mid.x, lo.x);
-                    split3(w * f[2], w * f[3], hi.y, mid.y, lo.y);
-                    split3(w * f[4], w * f[5], hi.z, mid.z, lo.z);
-                    split3(w * f[6], w * f[7], hi.w, mid.w, lo.w);
-                    uint8_t *q = prow + ((b ^ (k & 7)) << 4);
-                    *reinterpret_cast<uint4 *>(q) = hi;
-                    *reinterpret_cast<uint4 *>(q + kAtom) = mid;
-                    *reinterpret_cast<uint4 *>(q + 2 * kAtom) = lo;
-                }
-            } else {  // past the end: zero, whatever memory holds there
-                const uint4 z = make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int b = 0; b < 8; ++b) {
-                    reinterpret_cast<uint4 *>(crow)[b] = z;
-                    for (int t = 0; t < 3; ++t) reinterpret_cast<uint4 *>(prow + t * kAtom)[b] = z;
-                    for (int t = 0; t < na; ++t)
-                        reinterpret_cast<uint4 *>(sm + SM::B + (ib * 2 + t) * kAtom + k * 128)[b] = z;
-                }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(cready);
-                if (MODE != kStateOnly) mbar_arrive(&freeC[ic]);
-            }
-            ok = ok && mbar_wait_bounded(sfull, cc & 1, kSpinTc, err);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                float hi[16], mid[16];
-                tmem_ld16(tmem + TM::SD + lb + 16 * b, hi);
-                tmem_ld16(tmem + TM::SD + kN + lb + 16 * b, mid);
-                if (TM::SDW == 192) {
-                    float lo[16];
-                    tmem_ld16(tmem + TM::SD + 2 * kN + lb + 16 * b, lo);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int u = 0; u < 16; ++u) mid[u] += lo[u];
-                } else {
-                    tmem_wait_ld();
-                }
-#pragma unroll
-                for (int u = 0; u < 16; ++u) x[16 * b + u] = fmaf(dec, x[16 * b + u], hi[u] + mid[u]);
-            }
-            tc_fence_before();
-            // the products with X of this chunk are done (issued before the state's)
-            if (MODE != kStateOnly && cc + 1 < nch) publish();
         }
         if (ok && p.xout && k < p.db && (MODE == kStateOnly || last)) {
             float *dst = p.xout + (MODE == kStateOnly ? (size_t)slot * geo.H + h : (size_t)sl.z * geo.H + h) * nel;
             if (p.tr) {
 #pragma unroll
-                for (int u = 0; u < 16; ++u)
-                    if (c0 + 4 * u < p.dc)
-                        *reinterpret_cast<float4 *>(dst + (size_t)k * p.dc + c0 + 4 * u) =
+                for (int u = 0; u < 8; ++u)
+                    if (cx + 4 * u < p.dc)
+                        *reinterpret_cast<float4 *>(dst + (size_t)k * p.dc + cx + 4 * u) =
                             make_float4(x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]);
             } else {
 #pragma unroll
-                for (int u = 0; u < 64; ++u)
-                    if (c0 + u < p.dc) dst[(size_t)(c0 + u) * p.db + k] = x[u];
+                for (int u = 0; u < 32; ++u)
+                    if (cx + u < p.dc) dst[(size_t)(cx + u) * p.db + k] = x[u];
             }
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) tmem_dealloc(tmem, TM::COLS);
+    if (warp == 16) tmem_dealloc(tmem, TM::COLS);
 }
-
 
 // ------------------------------------------------------------ pairs inside a chunk, for dg
 // M = (Q K^T) . (dO V^T) . Gamma below the diagonal: row sums (the pairs' part of
@@ -684,17 +853,15 @@ struct PairArgs {
     float *rsum, *csum;  // [rows, H]
     int H_k, dk, dv;
 };
-constexpr int kPairTab = 704 + 8;
 struct PairSmem {
     static constexpr uint32_t QK = 0, VO = 4 * kAtom, TAB = 8 * kAtom;
-    static constexpr uint32_t BARS = TAB + 2 * kPairTab * 4, TOTAL = BARS + 8 * 8 + 16;
+    static constexpr uint32_t BARS = TAB + 2 * kTab * 4, TOTAL = BARS + 8 * 8 + 16;
 };
 
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__(kPairThreads, 1)
 pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
             const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
             PairArgs p, Geo geo, Plan plan, unsigned int *err) {
-    using SM = TcSmem<kOut>;  // table layout
     extern __shared__ __align__(1024) uint8_t sm[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + PairSmem::BARS);
     uint64_t *fullQ = bars, *fullV = bars + 1, *mdone = bars + 2, *tfull = bars + 3, *tfree = bars + 4;
@@ -733,14 +900,14 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             int it = 0;
             for (int cc = blockIdx.y; cc < nch; cc += gridDim.y, ++it) {
                 const int y = t0 + cc * kQ;
-                if (it) ok = mbar_wait_bounded(qdone, (it - 1) & 1, kSpinTc, err);
+                if (it) ok = wait(qdone, (it - 1) & 1, err);
                 if (!ok) break;
                 mbar_arrive_expect_tx(fullQ, 2 * nk * kAtom);
                 for (int i = 0; i < nk; ++i) {
                     tma_load_3d(sm + PairSmem::QK + i * kAtom, &tm_q, fullQ, 64 * i, hk, y);
                     tma_load_3d(sm + PairSmem::QK + (2 + i) * kAtom, &tm_k, fullQ, 64 * i, hk, y);
                 }
-                if (it) ok = mbar_wait_bounded(mdone, (it - 1) & 1, kSpinTc, err);
+                if (it) ok = wait(mdone, (it - 1) & 1, err);
                 if (!ok) break;
                 mbar_arrive_expect_tx(fullV, 2 * nv * kAtom);
                 for (int i = 0; i < nv; ++i) {
@@ -749,35 +916,33 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 }
             }
             if (it) {  // the last loads have landed and been read
-                mbar_wait_bounded(qdone, (it - 1) & 1, kSpinTc, err);
-                mbar_wait_bounded(mdone, (it - 1) & 1, kSpinTc, err);
+                wait(qdone, (it - 1) & 1, err);
+                wait(mdone, (it - 1) & 1, err);
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t id = idesc_bf16(128, 128, 0, 0);
-            const uint64_t dq = sdesc_sw128(smem_u32(sm + PairSmem::QK), 16, 1024);
-            const uint64_t dv = sdesc_sw128(smem_u32(sm + PairSmem::VO), 16, 1024);
-            int it = 0;
-            // columns: Q K^T 0, K Q^T 128, dO V^T 256, V dO^T 384
-            auto both = [&](uint64_t d, int ks, uint32_t col) {
-                for (int kk = 0; kk < ks; ++kk) {
-                    const uint32_t o = (kk >> 2) * kAtom + (kk & 3) * 32;
-                    mma_bf16_ss(tmem + col, sdesc_add(d, o), sdesc_add(d, 2 * kAtom + o), id, kk > 0);
-                    mma_bf16_ss(tmem + col + 128, sdesc_add(d, 2 * kAtom + o), sdesc_add(d, o), id, kk > 0);
-                }
-            };
-            for (int cc = blockIdx.y; cc < nch && ok; cc += gridDim.y, ++it) {
-                if (it) ok = mbar_wait_bounded(efree, (it - 1) & 1, kSpinTc, err);
-                ok = ok && mbar_wait_bounded(fullQ, it & 1, kSpinTc, err);
+        const uint32_t el = elect_lane(), id = idesc_bf16(128, 128, 0, 0);
+        const uint64_t dq = sdesc_sw128(smem_u32(sm + PairSmem::QK), 16, 1024);
+        const uint64_t dv = sdesc_sw128(smem_u32(sm + PairSmem::VO), 16, 1024);
+        int it = 0;
+        // columns: Q K^T 0, K Q^T 128, dO V^T 256, V dO^T 384
+        for (int cc = blockIdx.y; cc < nch && ok; cc += gridDim.y, ++it) {
+            if (it) ok = wait(efree, (it - 1) & 1, err);
+#pragma unroll 1
+            for (int m = 0; m < 2 && ok; ++m) {
+                ok = ok && wait(m ? fullV : fullQ, it & 1, err);
+                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                both(dq, p.dk / 16, 0);
-                mma_commit(qdone);
-                ok = ok && mbar_wait_bounded(fullV, it & 1, kSpinTc, err);
-                if (!ok) break;
-                both(dv, p.dv / 16, 256);
-                mma_commit(mdone);
+                const int ks = (m ? p.dv : p.dk) / 16;
+                const uint64_t d = m ? dv : dq;
+#pragma unroll 2
+                for (int kk = 0; kk < ks; ++kk) {
+                    const uint64_t x = sdesc_add(d, (kk >> 2) * kAtom + (kk & 3) * 32), y = sdesc_add(x, 2 * kAtom);
+                    mma_ss(el, tmem + 256 * m, x, y, id, kk > 0);
+                    mma_ss(el, tmem + 256 * m + 128, y, x, id, kk > 0);
+                }
+                commit(el, m ? mdone : qdone);
             }
         }
     } else if (warp < 4) {  // decays: warp 2 for the rows, warp 3 for the columns
@@ -791,14 +956,14 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         };
         load(blockIdx.y);
         for (int cc = blockIdx.y; cc < nch; cc += gridDim.y, ++it) {
-            if (it) ok = mbar_wait_bounded(tfree, (it - 1) & 1, kSpinTc, err);
+            if (it) ok = wait(tfree, (it - 1) & 1, err);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            float *tab = reinterpret_cast<float *>(sm + PairSmem::TAB) + (warp - 2) * kPairTab;
+            float *tab = reinterpret_cast<float *>(sm + PairSmem::TAB) + (warp - 2) * kTab;
             if (warp == 2)
-                decay_tables<false, SM>(tab, gv, min(kQ, len - cc * kQ), lane);
+                decay_tables<false>(tab, gv, lane);
             else
-                decay_tables<true, SM>(tab, gv, min(kQ, len - cc * kQ), lane);
+                decay_tables<true>(tab, gv, lane);
             __syncwarp();
             if (lane == 0) mbar_arrive(tfull);
             if (cc + (int)gridDim.y < nch) load(cc + gridDim.y);
@@ -807,46 +972,48 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         const bool rev = warp >= 8;
         const int rb = warp & 3, i = rb * 32 + lane;
         const uint32_t lb = (uint32_t)(rb * 32) << 16, col = rev ? 128 : 0;
-        const float *tab = reinterpret_cast<const float *>(sm + PairSmem::TAB) + (rev ? kPairTab : 0);
+        const float *tab = reinterpret_cast<const float *>(sm + PairSmem::TAB) + (rev ? kTab : 0);
         int it = 0;
         for (int cc = blockIdx.y; cc < nch; cc += gridDim.y, ++it) {
             const int n = min(kQ, len - cc * kQ);
-            ok = ok && mbar_wait_bounded(tfull, it & 1, kSpinTc, err);
-            ok = ok && mbar_wait_bounded(qdone, it & 1, kSpinTc, err);
-            ok = ok && mbar_wait_bounded(mdone, it & 1, kSpinTc, err);
+            ok = ok && wait(tfull, it & 1, err);
+            ok = ok && wait(qdone, it & 1, err);
+            ok = ok && wait(mdone, it & 1, err);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
-            const float li = tab[SM::LC + i];
+            const float li = tab[kLC + i];
+            const float rf = rev ? row_factor<true>(tab, rb, li) : row_factor<false>(tab, rb, li);
             float s = 0.f;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                if (rev ? b < rb : b > rb) continue;
-                float x[32], y[32];
-                tmem_ld16(tmem + col + lb + 32 * b, x);
-                tmem_ld16(tmem + col + lb + 32 * b + 16, x + 16);
-                tmem_ld16(tmem + 256 + col + lb + 32 * b, y);
-                tmem_ld16(tmem + 256 + col + lb + 32 * b + 16, y + 16);
-                tmem_wait_ld();
+#pragma unroll 1
+            for (int b = rev ? rb : 0; b <= (rev ? 3 : rb); ++b) {
                 float r = 0.f;
-                if (b == rb) {
+#pragma unroll 1
+                for (int c = 32 * b; c < 32 * b + 32; c += 16) {
+                    float x[16], y[16];
+                    tmem_ld16(tmem + col + lb + c, x);
+                    tmem_ld16(tmem + 256 + col + lb + c, y);
+                    tmem_wait_ld();
+                    const int at = c - 32 * b;
 #pragma unroll
-                    for (int u = 0; u < 32; ++u) {
-                        const float lj = tab[SM::LC + 32 * b + u];
-                        const bool in = rev ? u > lane && 32 * b + u < n : u < lane;
-                        r += in ? x[u] * y[u] * ex2(rev ? lj - li : li - lj) : 0.f;
-                    }
-                } else {
-                    const int hiB = rev ? b : rb, loB = rev ? rb : b;
-                    const float f = tab[SM::RF + (hiB * (hiB - 1) / 2 + loB) * 32 + lane];
+                    for (int u4 = 0; u4 < 4; ++u4) {
+                        const float4 l = *reinterpret_cast<const float4 *>(tab + (b == rb ? kLC : kCF) + c + 4 * u4);
+                        const float t[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
-                    for (int u = 0; u < 32; ++u) {
-                        const float z = x[u] * y[u] * tab[SM::CF + 32 * b + u];
-                        r += 32 * b + u < n ? z : 0.f;
+                        for (int v = 0; v < 4; ++v) {
+                            const int u = 4 * u4 + v;
+                            bool in = c + u < n;
+                            float f = t[v];
+                            if (b == rb) {
+                                in = rev ? in && at + u > lane : at + u < lane;
+                                f = ex2(rev ? f - li : li - f);
+                            }
+                            r += in ? x[u] * y[u] * f : 0.f;
+                        }
                     }
-                    r *= f;
                 }
-                s += r;
+                const int hiB = rev ? b : rb, loB = rev ? rb : b;
+                s = b == rb ? s + r : fmaf(r, rf * tab[kBB + hiB * (hiB - 1) / 2 + loB], s);
             }
             tc_fence_before();
             __syncwarp();
@@ -871,7 +1038,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 // of the carry.  S_end, dS_end at the end of the sequence.
 struct DgArgs {
     const float *ri, *ci, *rp, *cp;
-    int nri, nci;               // column groups of ri, ci
+    int nri, nci;               // planes of ri, ci
     const float *fin, *dfin;    // S_end, dS_end, or dfin NULL
     float *dg, *part;
     int nel;
@@ -1034,8 +1201,8 @@ TcWs tc_ws(const LinCall &c, bool bwd) {
     if (bwd) {
         w.Y = take(w.multi ? sh * nel * 4 : 0);
         w.fin = take((size_t)n_seq * c.H * nel * 4);
-        w.ri = take(rows * c.H * gk * 4);
-        w.ci = take(rows * c.H * gk * 4);
+        w.ri = take(rows * c.H * 2 * gk * 4);
+        w.ci = take(rows * c.H * 2 * gk * 4);
         w.rp = take(rows * c.H * 4);
         w.cp = take(rows * c.H * 4);
         w.dq32 = take(c.Hk < c.H ? rows * c.H * c.dk_ * 4 : 0);
@@ -1140,6 +1307,7 @@ cudaError_t lin_bwd_tc(const LinCall &c) {
     cudaError_t e;
     if ((e = lin_plan(c, geo, l)) != cudaSuccess) return e;
     const bool shared = c.Hk < c.H;
+    const __nv_bfloat16 *q = (const __nv_bfloat16 *)c.q, *k = (const __nv_bfloat16 *)c.k;
     float *X = (float *)(c.ws + w.X), *Y = (float *)(c.ws + w.Y), *fin = (float *)(c.ws + w.fin);
     float *ri = (float *)(c.ws + w.ri), *ci = (float *)(c.ws + w.ci);
     float *rp = (float *)(c.ws + w.rp), *cp = (float *)(c.ws + w.cp);
@@ -1167,7 +1335,7 @@ cudaError_t lin_bwd_tc(const LinCall &c) {
     p.xin = w.multi ? X : c.S0;
     p.xout = c.dS_final ? fin : nullptr;
     p.out = shared ? (void *)(c.ws + w.dq32) : c.dq;
-    p.e = (const __nv_bfloat16 *)c.q;
+    p.e = q;
     p.dots = ri;
     if ((e = launch_chain<false, kOutDots>(c, geo, plan, m.o, m.v, m.k, p, GDR_K_LIN_GRAD)) != cudaSuccess)
         return e;
@@ -1175,7 +1343,7 @@ cudaError_t lin_bwd_tc(const LinCall &c) {
     p.xin = w.multi ? Y : c.dS_final;
     p.xout = nullptr;
     p.out = shared ? (void *)(c.ws + w.dk32) : c.dk;
-    p.e = (const __nv_bfloat16 *)c.k;
+    p.e = k;
     p.dots = ci;
     if ((e = launch_chain<true, kOutDots>(c, geo, plan, m.v, m.o, m.q, p, GDR_K_LIN_GRAD)) != cudaSuccess)
         return e;
@@ -1196,15 +1364,24 @@ cudaError_t lin_bwd_tc(const LinCall &c) {
                                   (int)PairSmem::TOTAL)) != cudaSuccess)
         return e;
     const long units = (long)geo.n_slots * geo.H, most = w.L / kQ;
-    long split = (4 * 148 + units - 1) / units;
-    if (split > most) split = most;
+    // chunks of a (slot, head) per CTA: the number of CTAs that ends soonest on 148 SMs, a start
+    // costing about as much as one and a half chunks
+    long split = 1;
+    double least = 1e30;
+    for (long n = 1; n <= most && n <= 64; ++n) {
+        const double t = (double)((units * n + 147) / 148) * ((double)((most + n - 1) / n) + 1.5);
+        if (t < least) {
+            least = t;
+            split = n;
+        }
+    }
     PairArgs pa{c.g, rp, cp, c.Hk, c.dk_, c.dv_};
     ProfToken tk = prof_begin(GDR_K_LIN_GRAD, c.st);
-    pair_kernel<<<dim3((unsigned)units, (unsigned)split), kTcThreads, PairSmem::TOTAL, c.st>>>(
+    pair_kernel<<<dim3((unsigned)units, (unsigned)split), kPairThreads, PairSmem::TOTAL, c.st>>>(
         m.q, m.k, m.v, m.o, pa, geo, plan, c.err);
     prof_end(tk, c.st);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    DgArgs d{ri, ci, rp, cp, groups(c.dk_), groups(c.dk_), fin, c.dS_final, c.dg, part, c.dk_ * c.dv_};
+    DgArgs d{ri, ci, rp, cp, 2 * groups(c.dk_), 2 * groups(c.dk_), fin, c.dS_final, c.dg, part, c.dk_ * c.dv_};
     tk = prof_begin(GDR_K_LIN_GRAD, c.st);
     dg_chunks_kernel<<<(unsigned)(geo.n_seq * geo.H), 1024, 0, c.st>>>(d, c.cu, geo, plan);
     prof_end(tk, c.st);
