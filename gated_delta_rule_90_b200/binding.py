@@ -394,65 +394,79 @@ def bwd_linear_workspace_size(B, T, H, H_k, d_k, d_v, n_seq, varlen, dtype, gate
                                                    int(bool(varlen)), dtype, gate, PATHS[path]))
 
 
+def _linear_bad(dev, name, t, dtype, shape):
+    """Raise for a tensor that _linear_args does not take."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}; expected {dev}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {tuple(shape)}")
+    raise ValueError("tensors must be contiguous")
+
+
 def _linear_args(q, k, v, g, tensors):
     """Shapes and checks shared by the linear attention calls: q, k
     [*lead, H_k, d_k], v [*lead, H, d_v], g [*lead, H] or [H]; ``tensors`` are
     further ``(name, tensor, dtype, shape)``.  Every shape must match, every
-    tensor be contiguous and on q's device."""
-    dev = _on_cuda(q)
-    lead = q.shape[:-2]
-    (H_k, d_k), (H, d_v) = q.shape[-2:], v.shape[-2:]
+    tensor be contiguous and on q's device.  (A call for one token takes the
+    host about as long as the GPU: one expression per tensor, the message made
+    afterwards.)"""
+    if not (isinstance(q, torch.Tensor) and q.is_cuda):
+        raise ValueError("tensors must be CUDA tensors")
+    for name, t in (("v", v), ("g", g)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+    dev, qs, vs, tok = q.device, q.shape, v.shape, q.dtype
+    *lead, H_k, d_k = qs
+    H, d_v = vs[-2:]
     gate = GDR_GATE_HEAD if g.dim() == 1 else GDR_GATE_SCALAR
     if g.dim() == len(lead) + 2:
         raise ValueError("linear attention takes one decay per head ([..., H] or [H]), "
                          "not one per key channel")
     if H_k < 1 or H % H_k:
         raise ValueError(f"{H} value heads do not share {H_k} query/key heads evenly")
-    for name, t, dtype, shape in (("q", q, q.dtype, q.shape), ("k", k, q.dtype, q.shape),
-                                  ("v", v, q.dtype, (*lead, H, d_v)),
-                                  ("g", g, torch.float32, (H,) if gate else (*lead, H)), *tensors):
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}; expected {dev}")
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {tuple(shape)}")
-        if not t.is_contiguous():
-            raise ValueError("tensors must be contiguous")
+    for spec in (("q", q, tok, qs), ("k", k, tok, qs), ("v", v, tok, (*lead, H, d_v)),
+                 ("g", g, torch.float32, (H,) if gate else (*lead, H)), *tensors):
+        t = spec[1]
+        if t is not None and not (isinstance(t, torch.Tensor) and t.shape == spec[3] and
+                                  t.dtype == spec[2] and t.is_contiguous() and t.device == dev):
+            _linear_bad(dev, *spec)
     return dev, _dtype_code(q), gate, H, H_k, d_k, d_v
 
 
-def _linear_call(dev, stream, ws_bytes, workspace, shapes, call):
-    """Allocate what ``shapes`` asks for (``(tensor or None, shape or None,
-    dtype)``; given tensors are kept) and the workspace, then run ``call(made,
-    workspace, bytes, stream)`` with ``dev`` current.  Allocations belong to
-    the stream that the kernels run on, so that the allocator hands the
-    workspace to no other stream while they run."""
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _linear_call(dev, stream, ws_bytes, workspace, call):
+    """Run ``call(workspace address, bytes, stream handle)`` with ``dev`` current
+    and, where ``stream`` is given, that stream current too: what the call
+    allocates belongs to the stream that the kernels run on, so that the
+    allocator hands it to no other stream while they run."""
     if workspace is not None:
         _check(dev, ("workspace", workspace, None, 0))
         _need_contig(workspace)
-    handle = _stream(stream, dev)
 
-    def go():
-        made = [t if t is not None or shape is None else
-                torch.empty(shape, dtype=dtype, device=dev) for t, shape, dtype in shapes]
+    def go(handle):
         ws, n = workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
         if n < ws_bytes:
             ws, n = torch.empty(ws_bytes, dtype=torch.uint8, device=dev), ws_bytes
-        return made, call(made, ws, n, handle)
+        return call(_addr(ws), n, handle)
 
     if stream is not None:
+        handle = _stream(stream, dev).value or 0
         s = stream if isinstance(stream, torch.cuda.Stream) else \
-            torch.cuda.ExternalStream(handle.value or 0, device=dev)
+            torch.cuda.ExternalStream(handle, device=dev)
         with torch.cuda.device(dev), torch.cuda.stream(s):
-            return go()
+            return go(handle)
+    handle = torch._C._cuda_getCurrentRawStream(dev.index)
     if torch.cuda.current_device() == dev.index:
-        return go()
-    return _call_on(dev, go)
+        return go(handle)
+    with torch.cuda.device(dev):
+        return go(handle)
 
 
 def _linear_cu(cu_seqlens, B):
@@ -480,12 +494,17 @@ def gdr_fwd_linear(q, k, v, g, S0=None, *, cu_seqlens=None, out=None, S_final=No
         ("S_final", S_final, torch.float32, st_shape),
         ("cu_seqlens", cu_seqlens, torch.int32, (n_seq + 1,))))
     need = fwd_linear_workspace_size(B, T, H, H_k, d_k, d_v, n_seq, varlen, dtype, gate, path)
-    (out, S_final), st = _linear_call(
-        dev, stream, need, workspace,
-        ((out, v.shape, q.dtype), (S_final, st_shape if want_final else None, torch.float32)),
-        lambda made, ws, n, s: lib().gdr_fwd_linear(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S0), _ptr(made[0]), _ptr(made[1]), B, T, H, H_k,
-            d_k, d_v, _ptr(cu_seqlens), n_seq, dtype, gate, PATHS[path], _ptr(ws), n, s))
+
+    def call(ws, n, handle):
+        o = torch.empty_like(v) if out is None else out
+        sf = S_final
+        if sf is None and want_final:
+            sf = torch.empty(st_shape, dtype=torch.float32, device=dev)
+        return o, sf, lib().gdr_fwd_linear(
+            q.data_ptr(), _addr(k), v.data_ptr(), g.data_ptr(), _addr(S0), o.data_ptr(), _addr(sf),
+            B, T, H, H_k, d_k, d_v, _addr(cu_seqlens), n_seq, dtype, gate, PATHS[path], ws, n, handle)
+
+    out, S_final, st = _linear_call(dev, stream, need, workspace, call)
     if st != GDR_OK:
         raise GdrError(st, "gdr_fwd_linear")
     return out, S_final
@@ -499,11 +518,14 @@ def gdr_decode_step_linear(q, k, v, g, S, *, out=None, stream=None) -> torch.Ten
     dev, dtype, gate, H, H_k, d_k, d_v = _linear_args(q, k, v, g, (
         ("S", S, torch.float32, (N, v.shape[-2], v.shape[-1], q.shape[-1])),
         ("out", out, q.dtype, v.shape)))
-    (out,), st = _linear_call(
-        dev, stream, 0, None, ((out, v.shape, q.dtype),),
-        lambda made, ws, n, s: lib().gdr_decode_step_linear(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S), _ptr(made[0]), N, H, H_k, d_k, d_v, dtype,
-            gate, s))
+
+    def call(ws, n, handle):
+        o = torch.empty_like(v) if out is None else out
+        return o, lib().gdr_decode_step_linear(
+            q.data_ptr(), _addr(k), v.data_ptr(), g.data_ptr(), _addr(S), o.data_ptr(), N, H,
+            H_k, d_k, d_v, dtype, gate, handle)
+
+    out, st = _linear_call(dev, stream, 0, None, call)
     if st != GDR_OK:
         raise GdrError(st, "gdr_decode_step_linear")
     return out
@@ -525,17 +547,20 @@ def gdr_bwd_linear(q, k, v, g, dout, S0=None, dS_final=None, *, cu_seqlens=None,
         ("dk", dk, q.dtype, q.shape), ("dv", dv, q.dtype, v.shape), ("dg", dg, f32, g.shape),
         ("dS0", dS0, f32, st_shape), ("cu_seqlens", cu_seqlens, torch.int32, (n_seq + 1,))))
     need = bwd_linear_workspace_size(B, T, H, H_k, d_k, d_v, n_seq, varlen, dtype, gate, path)
-    made, st = _linear_call(
-        dev, stream, need, workspace,
-        ((dq, q.shape, q.dtype), (dk, q.shape, q.dtype), (dv, v.shape, q.dtype), (dg, g.shape, f32),
-         (dS0, st_shape if want_dS0 else None, f32)),
-        lambda made, ws, n, s: lib().gdr_bwd_linear(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S0), _ptr(dout), _ptr(dS_final),
-            *(_ptr(t) for t in made), B, T, H, H_k, d_k, d_v, _ptr(cu_seqlens), n_seq, dtype, gate,
-            PATHS[path], _ptr(ws), n, s))
+
+    def call(ws, n, handle):
+        made = (torch.empty_like(q) if dq is None else dq, torch.empty_like(q) if dk is None else dk,
+                torch.empty_like(v) if dv is None else dv, torch.empty_like(g) if dg is None else dg,
+                torch.empty(st_shape, dtype=f32, device=dev) if dS0 is None and want_dS0 else dS0)
+        return made, lib().gdr_bwd_linear(
+            q.data_ptr(), _addr(k), v.data_ptr(), g.data_ptr(), _addr(S0), _addr(dout),
+            _addr(dS_final), *(_addr(t) for t in made), B, T, H, H_k, d_k, d_v, _addr(cu_seqlens),
+            n_seq, dtype, gate, PATHS[path], ws, n, handle)
+
+    made, st = _linear_call(dev, stream, need, workspace, call)
     if st != GDR_OK:
         raise GdrError(st, "gdr_bwd_linear")
-    return tuple(made)
+    return made
 
 
 def device_status(stream=None) -> int:

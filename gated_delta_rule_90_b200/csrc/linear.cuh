@@ -6,6 +6,8 @@
 // (slot, head) as fp32 [d_v, d_k], like S itself.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace gdr {
@@ -42,6 +44,24 @@ __device__ __forceinline__ float load_g(const Geo &geo, const float *g, long row
 }  // namespace gdr
 
 namespace gdr_host {
+// A kernel's dynamic shared memory limit, set once on each device (the call costs
+// about as much as a launch).
+class SmemLimit {
+    std::atomic<unsigned long long> done_{0};
+
+public:
+    cudaError_t set(const void *kernel, int bytes) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+        if (done_.load(std::memory_order_acquire) & bit) return cudaSuccess;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess) done_.fetch_or(bit, std::memory_order_release);
+        return e;
+    }
+};
+
 // Arguments of one call, checked by the entry point.
 struct LinCall {
     const void *q, *k, *v, *dout;

@@ -384,7 +384,15 @@ Plan plan_of(const gdr_host::LinCall &c, const gdr_host::LinWs &w) {
 }
 
 gdr_host::LinWs simt_ws(const gdr_host::LinCall &c, bool bwd) {
-    return gdr_host::lin_ws(c.B, c.T, c.H, c.Hk, c.dk_, c.dv_, c.n_seq, c.cu != nullptr, bwd, kBlk,
+    // Blocks of up to 256 tokens; of fewer, down to one chunk, while the grid would leave SMs idle:
+    // a block's chunks run one after another (T 100, H 4, d 64: XX us of 256, XX us of 32)
+    int L = kBlk;
+    while (L > kC) {
+        const double slots = c.cu ? (double)c.T / L + c.n_seq : (double)c.B * ((c.T + L - 1) / L);
+        if (slots * c.H * blocks_of(c.dv_) >= 2 * 148) break;
+        L /= 2;
+    }
+    return gdr_host::lin_ws(c.B, c.T, c.H, c.Hk, c.dk_, c.dv_, c.n_seq, c.cu != nullptr, bwd, L,
                             blocks_of(c.dk_) > blocks_of(c.dv_) ? blocks_of(c.dk_) : blocks_of(c.dv_));
 }
 
@@ -404,8 +412,8 @@ cudaError_t launch_out(const gdr_host::LinCall &c, const Geo &geo, const Plan &p
                        const Roles<T> &ro, const float *X, void *out, float *dots, int id) {
     if (!geo.n_slots) return cudaSuccess;
     const size_t smem = out_smem(ro.db);
-    cudaError_t e = cudaFuncSetAttribute(out_kernel<T, To, REV>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static gdr_host::SmemLimit limit;
+    const cudaError_t e = limit.set((const void *)out_kernel<T, To, REV>, (int)out_smem(128));
     if (e != cudaSuccess) return e;
     gdr_host::ProfToken tk = gdr_host::prof_begin(id, c.st);
     out_kernel<T, To, REV><<<dim3(geo.n_slots, c.H, blocks_of(ro.dc)), kThreads, smem, c.st>>>(

@@ -36,7 +36,7 @@ constexpr int kQ = 128;                  // tokens of a chunk
 constexpr int kN = 64;                   // columns of c of a CTA
 constexpr uint32_t kSpinTc = 1u << 24;   // poll limit of every mbarrier wait
 constexpr int kTcThreads = 640;          // 8 output warps, 8 state warps, TMA and decays, 3 MMA issuers
-constexpr int kPairThreads = 384;        // TMA, MMA, decays of rows and columns; 4 warps each for their sums
+constexpr int kPairThreads = 640;        // TMA, MMA, decays of rows and columns; 8 warps each for their sums
 constexpr uint32_t kAtom = kQ * 128;     // bytes of 128 rows of 64 bf16
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -850,7 +850,7 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
 // less than summing over lanes.  Reads q, k, v, dout once: HBM-bound.
 struct PairArgs {
     const float *g;
-    float *rsum, *csum;  // [rows, H]
+    float *rsum, *csum;  // [2, rows, H]
     int H_k, dk, dv;
 };
 struct PairSmem {
@@ -881,8 +881,8 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         mbar_init(qdone, 1);
         mbar_init(mdone, 1);
         mbar_init(tfull, 2);
-        mbar_init(tfree, 8);
-        mbar_init(efree, 8);
+        mbar_init(tfree, 16);
+        mbar_init(efree, 16);
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -969,8 +969,9 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             if (cc + (int)gridDim.y < nch) load(cc + gridDim.y);
         }
     } else {
-        const bool rev = warp >= 8;
-        const int rb = warp & 3, i = rb * 32 + lane;
+        // rows (warps 4-11) or columns (12-19); two warps share a row's columns, 16 of each block each
+        const bool rev = warp >= 12;
+        const int rb = warp & 3, hf = ((warp - 4) >> 2) & 1, i = rb * 32 + lane;
         const uint32_t lb = (uint32_t)(rb * 32) << 16, col = rev ? 128 : 0;
         const float *tab = reinterpret_cast<const float *>(sm + PairSmem::TAB) + (rev ? kTab : 0);
         int it = 0;
@@ -987,31 +988,37 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             float s = 0.f;
 #pragma unroll 1
             for (int b = rev ? rb : 0; b <= (rev ? 3 : rb); ++b) {
-                float r = 0.f;
-#pragma unroll 1
-                for (int c = 32 * b; c < 32 * b + 32; c += 16) {
-                    float x[16], y[16];
-                    tmem_ld16(tmem + col + lb + c, x);
-                    tmem_ld16(tmem + 256 + col + lb + c, y);
-                    tmem_wait_ld();
-                    const int at = c - 32 * b;
+                const int c = 32 * b + 16 * hf;
+                float x[16], y[16], f[16];
+                tmem_ld16(tmem + col + lb + c, x);
+                tmem_ld16(tmem + 256 + col + lb + c, y);
 #pragma unroll
-                    for (int u4 = 0; u4 < 4; ++u4) {
-                        const float4 l = *reinterpret_cast<const float4 *>(tab + (b == rb ? kLC : kCF) + c + 4 * u4);
-                        const float t[4] = {l.x, l.y, l.z, l.w};
+                for (int u = 0; u < 16; u += 4) {
+                    const float4 l = *reinterpret_cast<const float4 *>(tab + (b == rb ? kLC : kCF) + c + u);
+                    f[u] = l.x; f[u + 1] = l.y; f[u + 2] = l.z; f[u + 3] = l.w;
+                }
+                tmem_wait_ld();
+                float r0 = 0.f, r1 = 0.f;
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            const int u = 4 * u4 + v;
-                            bool in = c + u < n;
-                            float f = t[v];
-                            if (b == rb) {
-                                in = rev ? in && at + u > lane : at + u < lane;
-                                f = ex2(rev ? f - li : li - f);
-                            }
-                            r += in ? x[u] * y[u] * f : 0.f;
-                        }
+                for (int u = 0; u < 16; u += 2) mul2(x[u], x[u + 1], y[u], y[u + 1]);
+                if (b == rb || c + 16 > n) {  // selects: what lies outside cannot matter
+#pragma unroll
+                    for (int u = 0; u < 16; ++u) {
+                        const int at = u + 16 * hf;
+                        const bool in = c + u < n && (b != rb || (rev ? at > lane : at < lane));
+                        if (b == rb) f[u] = ex2(rev ? f[u] - li : li - f[u]);
+                        x[u] = in ? x[u] * f[u] : 0.f;
+                    }
+#pragma unroll
+                    for (int u = 0; u < 16; u += 2) add2(r0, r1, x[u], x[u + 1]);
+                } else {
+#pragma unroll
+                    for (int u = 0; u < 16; u += 2) {
+                        mul2(x[u], x[u + 1], f[u], f[u + 1]);
+                        add2(r0, r1, x[u], x[u + 1]);
                     }
                 }
+                const float r = r0 + r1;
                 const int hiB = rev ? b : rb, loB = rev ? rb : b;
                 s = b == rb ? s + r : fmaf(r, rf * tab[kBB + hiB * (hiB - 1) / 2 + loB], s);
             }
@@ -1021,7 +1028,8 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 mbar_arrive(efree);
                 mbar_arrive(tfree);
             }
-            if (i < n) (rev ? p.csum : p.rsum)[((size_t)t0 + cc * kQ + i) * geo.H + h] = s;
+            if (i < n)
+                (rev ? p.csum : p.rsum)[(size_t)hf * geo.rows * geo.H + ((size_t)t0 + cc * kQ + i) * geo.H + h] = s;
         }
     }
     tc_fence_before();
@@ -1085,7 +1093,7 @@ dg_chunks_kernel(DgArgs p, const int32_t *__restrict__ cu, Geo geo, Plan plan) {
             const size_t at = ((size_t)t0 + i) * geo.H + h, pl = (size_t)geo.rows * geo.H;
             for (int u = 0; u < p.nri; ++u) y += p.ri[u * pl + at];
             for (int u = 0; u < p.nci; ++u) y -= p.ci[u * pl + at];
-            x = y + ((double)p.rp[at] - (double)p.cp[at]);
+            x = y + (((double)p.rp[at] + p.rp[pl + at]) - ((double)p.cp[at] + p.cp[pl + at]));
         }
         double ys = y;
 #pragma unroll
@@ -1203,8 +1211,8 @@ TcWs tc_ws(const LinCall &c, bool bwd) {
         w.fin = take((size_t)n_seq * c.H * nel * 4);
         w.ri = take(rows * c.H * 2 * gk * 4);
         w.ci = take(rows * c.H * 2 * gk * 4);
-        w.rp = take(rows * c.H * 4);
-        w.cp = take(rows * c.H * 4);
+        w.rp = take(rows * c.H * 2 * 4);
+        w.cp = take(rows * c.H * 2 * 4);
         w.dq32 = take(c.Hk < c.H ? rows * c.H * c.dk_ * 4 : 0);
         w.dk32 = take(c.Hk < c.H ? rows * c.H * c.dk_ * 4 : 0);
         w.part = take((size_t)n_seq * c.H * 4);
@@ -1248,8 +1256,8 @@ template <bool REV, int MODE>
 cudaError_t launch_chain(const LinCall &c, const Geo &geo, const Plan &plan, const CUtensorMap &a,
                          const CUtensorMap &b, const CUtensorMap &cc, TcArgs p, int id) {
     const size_t smem = TcSmem<MODE>::TOTAL;
-    cudaError_t e = cudaFuncSetAttribute(chain_kernel<REV, MODE>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static gdr_host::SmemLimit limit;
+    const cudaError_t e = limit.set((const void *)chain_kernel<REV, MODE>, (int)smem);
     if (e != cudaSuccess) return e;
     p.g = c.g;
     p.ng = groups(p.dc);
@@ -1360,9 +1368,8 @@ cudaError_t lin_bwd_tc(const LinCall &c) {
         if ((e = lin_group_sum(c, geo, l, (const float *)(c.ws + w.dq32), c.dq, c.dk_)) != cudaSuccess) return e;
         if ((e = lin_group_sum(c, geo, l, (const float *)(c.ws + w.dk32), c.dk, c.dk_)) != cudaSuccess) return e;
     }
-    if ((e = cudaFuncSetAttribute(pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  (int)PairSmem::TOTAL)) != cudaSuccess)
-        return e;
+    static SmemLimit limit;
+    if ((e = limit.set((const void *)pair_kernel, (int)PairSmem::TOTAL)) != cudaSuccess) return e;
     const long units = (long)geo.n_slots * geo.H, most = w.L / kQ;
     // chunks of a (slot, head) per CTA: the number of CTAs that ends soonest on 148 SMs, a start
     // costing about as much as one and a half chunks
