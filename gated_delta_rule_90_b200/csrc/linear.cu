@@ -88,7 +88,7 @@ scan_kernel(float *__restrict__ X, const float *__restrict__ gtot, const float *
     const int first = geo.varlen ? plan.blk_start[s] : s * geo.nb;
     const int nb = (geo.varlen ? plan.blk_start[s + 1] : first + geo.nb) - first;
     if (kChecked && !chk_span(first, nb, geo.n_slots, err)) return;
-    if (el >= nel) return;
+    if (el >= nel || (geo.skip_single && nb == 1)) return;
     const size_t so = ((size_t)s * geo.H + h) * nel + el;
     float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
     if (init) S = *reinterpret_cast<const float4 *>(init + so);

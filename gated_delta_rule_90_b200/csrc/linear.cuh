@@ -18,6 +18,7 @@ struct Geo {
     int L, nb, n_slots;                 // nb: blocks per sequence (equal lengths)
     int gate_head;                      // g is [H]: one log-decay for all tokens
     int keep_empty;                     // an empty packed sequence has one block of no tokens
+    int skip_single;                    // a sequence of one block takes its state from the caller's
 };
 
 // {first row, tokens, sequence, block}; a slot that no block fills has -1 tokens.

@@ -64,24 +64,26 @@ struct TcSmem {
     static_assert(TOTAL <= 227 * 1024, "shared memory");
 };
 
-// Tensor memory columns.  SD = (w C)^T B in two blocks, the first split term and
-// the other two: in one accumulator the small terms' steps round at the size of
-// the large one's sum (1.9e-7 of the state, against 6.5e-8 apart).  P is replaced
-// in place by its bf16 form (8 columns of each 16).  O = P C, OIN = A X^T: two
-// buffers each, so that a chunk's outputs are written after the next chunk's P,
-// whose products run meanwhile (LAG); with three terms of X, OIN has two blocks
-// and one buffer.
+// Tensor memory columns.  SD = (w C)^T B, a block per split term, in one product
+// 192 columns wide: an MMA took 74 cycles at up to 128 columns, 100 at 192, so three
+// of 64 cost 240; and added into one block, the small terms' steps round at the size
+// of the large one's sum (1.9e-7 of the state, against 6.5e-8 apart).  P is replaced
+// in place by its bf16 form (8 columns of each 16).  O = P C has two buffers, so that
+// a chunk's outputs are written after the next chunk's P, whose products run
+// meanwhile (LAG).  With three terms of X, OIN = A X^T takes two blocks (the first
+// term; the others) and O one buffer.
 template <int MODE>
 struct TcTmem {
     static constexpr bool DOTS = MODE == kOutDots;
-    static constexpr int LAG = DOTS ? 0 : 1, NBUF = LAG + 1;
-    static constexpr int SD = 0, P = 128, O = 256, OIN = 384;
-    static constexpr uint32_t COLS = MODE == kStateOnly ? 128 : 512;
+    static constexpr int LAG = DOTS ? 0 : 1;
+    static constexpr int SD = 0, P = 192, O = 320, OIN = DOTS ? 384 : 448;
+    static constexpr uint32_t COLS = MODE == kStateOnly ? 256 : 512;
 };
 
 struct TcArgs {
     const float *g;
-    const float *xin;    // state that enters: per (sequence, head), or per (slot, head) when `multi`
+    const float *xin;    // state that enters a sequence, or NULL (zero)
+    const float *xblk;   // state that enters a block of a sequence of several, per (slot, head)
     float *xout;         // state that leaves (per sequence), or the blocks' own states (state only)
     float *gtot;         // state only: the blocks' sums of log-decays
     void *out;           // bf16, or fp32 with out32
@@ -90,7 +92,6 @@ struct TcArgs {
     int ha, hb, hc, he;  // heads of a, b, c, e
     int db, dc, ng;      // widths, column groups
     int tr;              // states are stored as the transpose of X
-    int multi;           // more than one block per sequence
     int out32, wide;     // out is fp32; out is 32-byte aligned
 };
 
@@ -203,6 +204,14 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// A log-decay, unclamped: a clamp where it is loaded would make the warp wait for
+// the load there (3300 cycles a chunk), not where the value is needed.
+__device__ __forceinline__ float load_raw_g(const Geo &geo, const float *g, long row, int h) {
+    float x;
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(x) : "l"(geo.gate_head ? g + h : g + row * geo.H + h));
+    return x;
+}
+
 // A number in two floats, hi + lo (about 48 bits): sums by Knuth's exact two-sum.
 // The running sums of log-decays need it, for differences of far positions have to
 // be rounded once, not at the size of the sums.  In fp64 the sums took 6 times as
@@ -310,7 +319,7 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     uint64_t *fullA = bars, *fullB = bars + 2, *fullC = bars + 4;      // tile loaded
     uint64_t *freeA = bars + 6, *freeB = bars + 8, *freeC = bars + 10; // its readers are done
     uint64_t *pfull = bars + 12, *pready = bars + 14, *ofull = bars + 15;  // P and decays; its bf16 form; O
-    uint64_t *ifull = bars + 16, *ifree = bars + 18;                   // OIN; O and OIN written out
+    uint64_t *ifull = bars + 16, *ifree = bars + 17;                   // OIN; O and OIN written out
     uint64_t *cready = bars + 20;                   // [2] w C, tokens 0-63 and 64-127
     uint64_t *sfree = bars + 22, *sfull = bars + 23, *sdfree = bars + 24;  // first half done; SD
     uint64_t *xready = bars + 25, *tfree = bars + 26, *zready = bars + 28;
@@ -343,8 +352,6 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             mbar_init(&fullB[i], 1);
             mbar_init(&fullC[i], 2);  // the tile and the chunk's decays
             mbar_init(&pfull[i], 2);
-            mbar_init(&ifull[i], 1);
-            mbar_init(&ifree[i], 8);
             mbar_init(&freeA[i], 2);
             mbar_init(&freeB[i], MODE == kStateOnly ? 1 : 2);
             mbar_init(&freeC[i], MODE == kStateOnly ? 8 : 9);  // the 8 split warps; O = P C
@@ -353,6 +360,8 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         }
         mbar_init(pready, 8);
         mbar_init(ofull, 1);
+        mbar_init(ifull, 1);
+        mbar_init(ifree, 8);
         mbar_init(sfree, 1);
         mbar_init(sfull, 1);
         mbar_init(sdfree, 8);
@@ -383,7 +392,7 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             const int j0 = chunk_at(cc), n = min(kQ, len - j0);
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-                gv[u] = 4 * lane + u < n ? load_g(geo, p.g, (long)t0 + j0 + 4 * lane + u, h) : 0.f;
+                gv[u] = 4 * lane + u < n ? load_raw_g(geo, p.g, (long)t0 + j0 + 4 * lane + u, h) : 0.f;
         };
         Two tot = {0.f, 0.f};
         // the tiles of chunk cc, as their buffers fall free.  (The whole warp waits: with the waits
@@ -398,6 +407,12 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                     tma_load_3d(sm + SM::B + (i2 * 2 + i) * kAtom, &tm_b, &fullB[i2], 64 * i, hb, y);
             }
             __syncwarp();
+            if (cc >= 2) ok = ok && wait(&freeC[i2], (cc / 2 - 1) & 1, err);
+            if (ok && lane == 0) {
+                mbar_arrive_expect_tx(&fullC[i2], kAtom);
+                tma_load_3d(sm + SM::Cc + i2 * kAtom, &tm_c, &fullC[i2], c0, hc, y);
+            }
+            __syncwarp();
             if (MODE != kStateOnly) {
                 if (cc >= SM::NA) ok = ok && wait(&freeA[ia], (cc / SM::NA - 1) & 1, err);
                 if (ok && lane == 0) {
@@ -407,12 +422,6 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                 }
                 __syncwarp();
             }
-            if (cc >= 2) ok = ok && wait(&freeC[i2], (cc / 2 - 1) & 1, err);
-            if (ok && lane == 0) {
-                mbar_arrive_expect_tx(&fullC[i2], kAtom);
-                tma_load_3d(sm + SM::Cc + i2 * kAtom, &tm_c, &fullC[i2], c0, hc, y);
-            }
-            __syncwarp();
         };
         if (nch > 0) {
             load(0);
@@ -424,6 +433,8 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             if (cc >= 2) ok = ok && wait(&tfree[i2], (cc / 2 - 1) & 1, err);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) gv[u] = clamp_g(gv[u]);
             tot = add(tot, decay_tables<REV>(tabs + i2 * kTab, gv, lane));
             __syncwarp();
             if (lane == 0) {
@@ -485,44 +496,53 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             const int ks = p.db / 16;
             for (int cc = 0; cc < nch; ++cc) {
                 const int i2 = cc & 1, ia = SM::NA == 2 ? i2 : 0;
-                ok = ok && wait(&fullA[ia], (cc / SM::NA) & 1, err);
-                ok = ok && wait(xready, cc & 1, err);
-                if (cc >= TM::NBUF) ok = ok && wait(&ifree[cc % TM::NBUF], (cc / TM::NBUF - 1) & 1, err);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t da = sdesc_add(dA, ia * 2 * kAtom);
-                const uint32_t tI = tmem + TM::OIN + cc % TM::NBUF * kN, tO = tmem + TM::O + cc % TM::NBUF * kN;
+                // the product with X waits for the outputs of the chunk before: with LAG these come
+                // after P of this chunk, so O goes first; else X does, which frees the a tile early
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    if (kk < ks) {
-                        const uint64_t a = sdesc_add(da, (kk >> 2) * kAtom + (kk & 3) * 32);
-                        const uint64_t b = sdesc_add(dX, kk * 2048);
-                        mma_ss(el, tI, a, b, idN, kk > 0);
-                        if (TM::DOTS) {
-                            mma_ss(el, tI + kN, a, sdesc_add(b, kAtom), idN, kk > 0);
-                            mma_ss(el, tI + kN, a, sdesc_add(b, 2 * kAtom), idN, 1);
-                        }
+                for (int step = 0; step < 2; ++step) {
+                    if (step == (TM::LAG ? 0 : 1)) {
+                        ok = ok && wait(&fullC[i2], (cc >> 1) & 1, err);
+                        ok = ok && wait(pready, cc & 1, err);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t d = sdesc_add(dC, i2 * kAtom);
+                        const uint32_t tO = tmem + TM::O + (TM::LAG ? i2 * kN : 0);
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)
+                            mma_ts(el, tO, tmem + TM::P + kk * 16, sdesc_add(d, kk * 2048), idN, kk > 0);
+                        commit(el, &freeC[i2]);
+                        commit(el, ofull);
+                    } else {
+                        ok = ok && wait(&fullA[ia], (cc / SM::NA) & 1, err);
+                        ok = ok && wait(xready, cc & 1, err);
+                        if (cc > 0) ok = ok && wait(ifree, (cc - 1) & 1, err);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t da = sdesc_add(dA, ia * 2 * kAtom);
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)
+                            if (kk < ks) {
+                                const uint64_t a = sdesc_add(da, (kk >> 2) * kAtom + (kk & 3) * 32);
+                                const uint64_t b = sdesc_add(dX, kk * 2048);
+                                mma_ss(el, tmem + TM::OIN, a, b, idN, kk > 0);
+                                if (TM::DOTS) {
+                                    mma_ss(el, tmem + TM::OIN + kN, a, sdesc_add(b, kAtom), idN, kk > 0);
+                                    mma_ss(el, tmem + TM::OIN + kN, a, sdesc_add(b, 2 * kAtom), idN, 1);
+                                }
+                            }
+                        commit(el, &freeA[ia]);
+                        commit(el, ifull);
                     }
-                commit(el, &freeA[ia]);
-                commit(el, &ifull[cc % TM::NBUF]);
-                ok = ok && wait(&fullC[i2], (cc >> 1) & 1, err);
-                ok = ok && wait(pready, cc & 1, err);
-                ok = __all_sync(0xffffffffu, ok);
+                }
                 if (!ok) break;
-                tc_fence_after();
-                const uint64_t d = sdesc_add(dC, i2 * kAtom);
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_ts(el, tO, tmem + TM::P + kk * 16, sdesc_add(d, kk * 2048), idN, kk > 0);
-                commit(el, &freeC[i2]);
-                commit(el, ofull);
             }
         }
     } else if (warp == 19) {
         // ===================== MMA: SD = (w C)^T B, half the tokens at a time =====================
         {
-            const uint32_t el = elect_lane(), idS = idesc_bf16(128, kN, 1, 1);
+            const uint32_t el = elect_lane(), idS = idesc_bf16(128, 3 * kN, 1, 1);
             // b as [d_b, tokens]: with one 64-wide block the upper lanes repeat it (not read)
             const uint64_t dB = sdesc_sw128(smem_u32(sm + SM::B), na > 1 ? kAtom : 0, 1024);
             const uint64_t dP = sdesc_sw128(smem_u32(sm + SM::CP), kAtom, 1024);
@@ -538,12 +558,8 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
-                    for (int kk = 4 * hf; kk < 4 * hf + 4; ++kk) {
-                        const uint64_t a = sdesc_add(db, kk * 2048), b = sdesc_add(dP, kk * 2048);
-                        mma_ss(el, tmem + TM::SD, a, b, idS, kk > 0);
-                        mma_ss(el, tmem + TM::SD + kN, a, sdesc_add(b, kAtom), idS, kk > 0);
-                        mma_ss(el, tmem + TM::SD + kN, a, sdesc_add(b, 2 * kAtom), idS, 1);
-                    }
+                    for (int kk = 4 * hf; kk < 4 * hf + 4; ++kk)
+                        mma_ss(el, tmem + TM::SD, sdesc_add(db, kk * 2048), sdesc_add(dP, kk * 2048), idS, kk > 0);
                     if (hf == 0) commit(el, sfree);
                 }
                 if (!ok) break;
@@ -559,8 +575,18 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             const uint32_t lb = (uint32_t)(rb * 32) << 16;
             const int ncb = min(kN, p.dc - c0) >> 4;
             float eg = 0.f;  // weight of the state that entered chunk cc - 1
+            uint4 ev[4];     // DOTS: this row's 32 columns of e, asked for before P
             for (int cc = 0; cc < nch + TM::LAG; ++cc) {
                 float egn = 0.f;
+                if (MODE == kOutDots) {
+                    const int n = min(kQ, len - chunk_at(cc));
+                    const size_t row = (size_t)t0 + chunk_at(cc) + i;
+                    const __nv_bfloat16 *e = p.e + (row * p.he + h / (geo.H / p.he)) * p.dc + c0 + 32 * hf;
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        ev[u] = i < n && c0 + 32 * hf + 8 * u < p.dc ? __ldg(reinterpret_cast<const uint4 *>(e) + u)
+                                                                     : make_uint4(0, 0, 0, 0);
+                }
                 if (cc < nch) {
                     const float *tab = tabs + (cc & 1) * kTab;
                     ok = ok && wait(&pfull[cc & 1], (cc >> 1) & 1, err);
@@ -619,9 +645,9 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                     }
                 }
                 if (cc >= TM::LAG) {
-                    const int pc = cc - TM::LAG, ib = pc % TM::NBUF, j0 = chunk_at(pc), n = min(kQ, len - j0);
+                    const int pc = cc - TM::LAG, j0 = chunk_at(pc), n = min(kQ, len - j0);
                     const size_t row = (size_t)t0 + j0 + i;
-                    ok = ok && wait(&ifull[ib], (pc / TM::NBUF) & 1, err);
+                    ok = ok && wait(ifull, pc & 1, err);
                     // (with LAG, P of chunk cc was formed after this product)
                     if (!TM::LAG || cc == nch) ok = ok && wait(ofull, pc & 1, err);
                     if (!TM::LAG) eg = egn;
@@ -629,30 +655,27 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                     if (!ok) break;
                     tc_fence_after();
                     float d = 0.f;
-                    const __nv_bfloat16 *e = nullptr;
-                    if (MODE == kOutDots) e = p.e + (row * p.he + h / (geo.H / p.he)) * p.dc + c0;
                     const size_t at = (row * geo.H + h) * p.dc + c0;
-#pragma unroll 1
-                    for (int b = 2 * hf; b < min(ncb, 2 * hf + 2); ++b) {
+#pragma unroll
+                    for (int v = 0; v < 2; ++v) {
+                        const int b = 2 * hf + v;
+                        if (b >= ncb) break;
                         float o[16], y[16];
-                        tmem_ld16(tmem + TM::OIN + ib * kN + lb + 16 * b, o);
-                        tmem_ld16(tmem + TM::O + ib * kN + lb + 16 * b, y);
+                        tmem_ld16(tmem + TM::OIN + lb + 16 * b, o);
+                        tmem_ld16(tmem + TM::O + (TM::LAG ? (pc & 1) * kN : 0) + lb + 16 * b, y);
                         if (MODE == kOutDots) {
-                            float m[16];
+                            float m[16], f[16];
                             tmem_ld16(tmem + TM::OIN + kN + lb + 16 * b, m);
+                            unpack8(ev[2 * v], f);
+                            unpack8(ev[2 * v + 1], f + 8);
                             tmem_wait_ld();
 #pragma unroll
                             for (int u = 0; u < 16; u += 2) {
                                 add2(o[u], o[u + 1], m[u], m[u + 1]);
                                 mul2(o[u], o[u + 1], eg, eg);
                             }
-                            if (i < n) {
-                                float f[16];
-                                unpack8(*reinterpret_cast<const uint4 *>(e + 16 * b), f);
-                                unpack8(*reinterpret_cast<const uint4 *>(e + 16 * b + 8), f + 8);
 #pragma unroll
-                                for (int u = 0; u < 16; ++u) d = fmaf(o[u], f[u], d);
-                            }
+                            for (int u = 0; u < 16; ++u) d = fmaf(o[u], f[u], d);
 #pragma unroll
                             for (int u = 0; u < 16; u += 2) add2(y[u], y[u + 1], o[u], o[u + 1]);
                         } else {
@@ -683,7 +706,7 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                         p.dots[((size_t)(2 * ng + hf) * geo.rows + row) * geo.H + h] = d;
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&ifree[ib]);
+                    if (lane == 0) mbar_arrive(ifree);
                 }
                 eg = egn;
             }
@@ -696,9 +719,9 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         float x[32];
 #pragma unroll
         for (int u = 0; u < 32; ++u) x[u] = 0.f;
-        const size_t unit = (size_t)(p.multi ? slot : sl.z) * geo.H + h;
-        if (MODE != kStateOnly && p.xin && k < p.db) {
-            const float *src = p.xin + unit * nel;
+        const float *enter = nblk > 1 ? p.xblk : p.xin;
+        if (MODE != kStateOnly && enter && k < p.db) {
+            const float *src = enter + ((size_t)(nblk > 1 ? slot : sl.z) * geo.H + h) * nel;
             if (p.tr) {
 #pragma unroll
                 for (int u = 0; u < 8; ++u)
@@ -719,9 +742,14 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
             const int i2 = cc & 1, n = cc < nch ? min(kQ, len - chunk_at(cc)) : 0;
             const float *tab = tabs + i2 * kTab;
             float decn = 0.f;
+            // kOut: split of the first half, the state of the chunk before, the second half, so that the
+            // state's product runs meanwhile (95 us; the state first 103).  DOTS: the state first, for the
+            // a tile's buffer waits for the product with it (119 us; between the halves 128).
 #pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-                if (cc < nch) {
+            for (int step = 0; step < 3; ++step) {
+                const bool update = step == (MODE == kOutDots ? 0 : 1);
+                const int half = MODE == kOutDots ? step - 1 : step >> 1;
+                if (!update && cc < nch) {
                     if (half == 0) {
                         ok = ok && wait(&fullC[i2], (cc >> 1) & 1, err);
                         if (n < kQ) ok = ok && wait(&fullB[i2], (cc >> 1) & 1, err);
@@ -768,7 +796,7 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                         }
                     }
                 }
-                if (half == 0 && cc > 0) {  // X <- e^{G_n} X + SD of chunk cc - 1
+                if (update && cc > 0) {  // X <- e^{G_n} X + SD of chunk cc - 1
                     ok = ok && wait(sfull, (cc - 1) & 1, err);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
@@ -776,12 +804,14 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
 #pragma unroll
                     for (int b = 0; b < 4; ++b) {
                         const uint32_t col = tmem + TM::SD + lb + 32 * hf + 8 * b;
-                        float hi[8], mid[8];
+                        float hi[8], mid[8], lo[8];
                         tmem_ld8(col, hi);
                         tmem_ld8(col + kN, mid);
+                        tmem_ld8(col + 2 * kN, lo);
                         tmem_wait_ld();
 #pragma unroll
                         for (int u = 0; u < 8; u += 2) {
+                            add2(mid[u], mid[u + 1], lo[u], lo[u + 1]);
                             add2(hi[u], hi[u + 1], mid[u], mid[u + 1]);
                             fma2(hi[u], hi[u + 1], dec, x[8 * b + u], x[8 * b + u + 1]);
                             x[8 * b + u] = hi[u];
@@ -792,35 +822,36 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                     __syncwarp();
                     if (lane == 0) mbar_arrive(sdfree);
                 }
+                if (update && cc < nch && MODE != kStateOnly) {
+                    // X as the B operand of A X^T (row k, swizzled), once the last chunk's product is done
+                    if (cc > 0) {
+                        ok = ok && wait(ifull, (cc - 1) & 1, err);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                    }
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const uint32_t off = SM::X + k * 128 + (((4 * hf + b) ^ (k & 7)) << 4);
+                        if (MODE == kOutDots) {
+                            uint4 hi, mid, lo;
+                            split3(x[8 * b], x[8 * b + 1], hi.x, mid.x, lo.x);
+                            split3(x[8 * b + 2], x[8 * b + 3], hi.y, mid.y, lo.y);
+                            split3(x[8 * b + 4], x[8 * b + 5], hi.z, mid.z, lo.z);
+                            split3(x[8 * b + 6], x[8 * b + 7], hi.w, mid.w, lo.w);
+                            *reinterpret_cast<uint4 *>(sm + off) = hi;
+                            *reinterpret_cast<uint4 *>(sm + off + kAtom) = mid;
+                            *reinterpret_cast<uint4 *>(sm + off + 2 * kAtom) = lo;
+                        } else {
+                            *reinterpret_cast<uint4 *>(sm + off) = pack8(x + 8 * b);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(xready);
+                }
             }
             if (!ok) break;
             dec = decn;
-            if (MODE == kStateOnly || cc == nch) continue;
-            // X as the B operand of A X^T (row k, swizzled), once the last chunk's product is done
-            if (cc > 0) {
-                ok = ok && wait(&ifull[(cc - 1) % TM::NBUF], ((cc - 1) / TM::NBUF) & 1, err);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-            }
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const uint32_t off = SM::X + k * 128 + (((4 * hf + b) ^ (k & 7)) << 4);
-                if (MODE == kOutDots) {
-                    uint4 hi, mid, lo;
-                    split3(x[8 * b], x[8 * b + 1], hi.x, mid.x, lo.x);
-                    split3(x[8 * b + 2], x[8 * b + 3], hi.y, mid.y, lo.y);
-                    split3(x[8 * b + 4], x[8 * b + 5], hi.z, mid.z, lo.z);
-                    split3(x[8 * b + 6], x[8 * b + 7], hi.w, mid.w, lo.w);
-                    *reinterpret_cast<uint4 *>(sm + off) = hi;
-                    *reinterpret_cast<uint4 *>(sm + off + kAtom) = mid;
-                    *reinterpret_cast<uint4 *>(sm + off + 2 * kAtom) = lo;
-                } else {
-                    *reinterpret_cast<uint4 *>(sm + off) = pack8(x + 8 * b);
-                }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(xready);
         }
         if (ok && p.xout && k < p.db && (MODE == kStateOnly || last)) {
             float *dst = p.xout + (MODE == kStateOnly ? (size_t)slot * geo.H + h : (size_t)sl.z * geo.H + h) * nel;
@@ -1038,18 +1069,26 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 }
 
 // ------------------------------------------------------------ gradient of the decays
-// One CTA per (sequence, head), chunks from the last to the first, 8 at a time
-// (a warp group of 128 threads each), in 64 bits:
+// A CTA takes a run of chunks of a (sequence, head), from the last to the first, 8
+// at a time (128 threads each), in 64 bits:
 //     dg_t = sum_{l >= t in chunk} (R_l - C_l) + sum over later chunks (Ri - Ci) + <S_end, dS_end>,
 // R = Ri + Rp, C = Ci + Cp: the state's part (dots of the chains) and the part of
 // the chunk's own pairs, whose rows and columns sum to the same and so drop out
-// of the carry.  S_end, dS_end at the end of the sequence.
+// of the carry.  S_end, dS_end at the end of the sequence.  Up to 16 CTAs share a
+// sequence; each sums the later chunks' part itself, all loads at once, which takes
+// less than waiting for the one before (T 8192, H 4: 32 us by one CTA, XX us).
+__device__ __forceinline__ double warp_sum(double x) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+constexpr int kDgCtas = 16;  // CTAs of a sequence and head at most
 struct DgArgs {
     const float *ri, *ci, *rp, *cp;
     int nri, nci;               // planes of ri, ci
     const float *fin, *dfin;    // S_end, dS_end, or dfin NULL
     float *dg, *part;
-    int nel;
+    int nel, rounds;            // rounds of 8 chunks of a CTA
 };
 
 __global__ void __launch_bounds__(1024)
@@ -1076,28 +1115,43 @@ dg_chunks_kernel(DgArgs p, const int32_t *__restrict__ cu, Geo geo, Plan plan) {
             const float4 b = reinterpret_cast<const float4 *>(p.dfin + o)[i];
             acc = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, acc))));
         }
-        f = acc;
-#pragma unroll
-        for (int o2 = 16; o2; o2 >>= 1) f += __shfl_xor_sync(0xffffffffu, f, o2);
+        f = warp_sum((double)acc);
         if (lane == 0) red[warp] = f;
         __syncthreads();
-        f = 0.0;
-        for (int w = 0; w < 32; ++w) f += red[w];
+        f = warp_sum(red[lane]);
     }
     const int nch = (len + kQ - 1) / kQ, grp = tid >> 7, j = tid & 127;
+    const int top = nch - 1 - 8 * p.rounds * (int)blockIdx.y, bottom = max(top - 8 * p.rounds, -1);
     double all = 0.0, c0 = f;  // c0: the sum over the chunks behind
-    for (int base = nch - 1; base >= 0; base -= 8) {
+    if (top < 0) {             // nothing left for this CTA
+        if (p.part && tid == 0) p.part[(size_t)blockIdx.y * gridDim.x + blockIdx.x] = 0.f;
+        return;
+    }
+    if (blockIdx.y > 0) {
+        const size_t pl = (size_t)geo.rows * geo.H;
+        double y = 0.0;
+#pragma unroll 4
+        for (int i = (top + 1) * kQ + tid; i < len; i += 1024) {
+            const size_t at = ((size_t)t0 + i) * geo.H + h;
+            for (int u = 0; u < p.nri; ++u) y += p.ri[u * pl + at];
+            for (int u = 0; u < p.nci; ++u) y -= p.ci[u * pl + at];
+        }
+        y = warp_sum(y);
+        __syncthreads();
+        if (lane == 0) red[warp] = y;
+        __syncthreads();
+        c0 += warp_sum(red[lane]);
+    }
+    for (int base = top; base > bottom; base -= 8) {
         const int cc = base - grp, i = cc * kQ + j;
         double x = 0.0, y = 0.0;  // everything; the state's part
-        if (cc >= 0 && i < len) {
+        if (cc > bottom && i < len) {
             const size_t at = ((size_t)t0 + i) * geo.H + h, pl = (size_t)geo.rows * geo.H;
             for (int u = 0; u < p.nri; ++u) y += p.ri[u * pl + at];
             for (int u = 0; u < p.nci; ++u) y -= p.ci[u * pl + at];
             x = y + (((double)p.rp[at] + p.rp[pl + at]) - ((double)p.cp[at] + p.cp[pl + at]));
         }
-        double ys = y;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) ys += __shfl_xor_sync(0xffffffffu, ys, o);
+        const double ys = warp_sum(y);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {  // inclusive sum from the warp's end
             const double z = __shfl_down_sync(0xffffffffu, x, o);
@@ -1109,12 +1163,10 @@ dg_chunks_kernel(DgArgs p, const int32_t *__restrict__ cu, Geo geo, Plan plan) {
             inter[warp] = ys;
         }
         __syncthreads();
-        double add = c0;
-        for (int w = 0; w < 4 * grp; ++w) add += inter[w];  // groups behind this chunk
-        for (int w = warp + 1; w < 4 * grp + 4; ++w) add += tot[w];
-        x += add;
-        for (int w = 0; w < 32; ++w) c0 += inter[w];
-        if (cc >= 0 && i < len) {
+        // the chunks behind this one, and this chunk's warps behind
+        x += c0 + warp_sum((lane < 4 * grp ? inter[lane] : 0.0) + (lane > warp && lane < 4 * grp + 4 ? tot[lane] : 0.0));
+        c0 += warp_sum(inter[lane]);
+        if (cc > bottom && i < len) {
             if (p.part)
                 all += x;
             else
@@ -1122,16 +1174,12 @@ dg_chunks_kernel(DgArgs p, const int32_t *__restrict__ cu, Geo geo, Plan plan) {
         }
     }
     if (!p.part) return;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    all = warp_sum(all);
     __syncthreads();
     if (lane == 0) red[warp] = all;
     __syncthreads();
-    if (tid == 0) {
-        double r = 0.0;
-        for (int w = 0; w < 32; ++w) r += red[w];
-        p.part[blockIdx.x] = (float)r;
-    }
+    all = warp_sum(red[lane]);
+    if (tid == 0) p.part[(size_t)blockIdx.y * gridDim.x + blockIdx.x] = (float)all;
 }
 
 }  // namespace lin
@@ -1148,30 +1196,32 @@ int groups(int d) { return (d + kN - 1) / kN; }
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Tokens of a block: a whole sequence while the (sequence, head, column group)
-// walks fill the GPU, else pieces of it.  Pieces cost a pass over k and v for
-// their states and the carry, so equal sequences are cut where the estimate
-// below says that it pays (about 1.5 us for a chunk of a walk, 0.9 us without
-// outputs, 148 walks at a time), and packed ones, whose lengths the host does
-// not know, into what one SM's share of all tokens is.
-int block_len(int n_seq, bool varlen, int B, int T, int H, int ng, size_t nel) {
+// walks fill the GPU, else pieces of it.  Pieces cost a pass for their states and
+// the carry, so equal sequences are cut where the estimate below says that it pays:
+// one walk to an SM, a chunk of one 2.6 us and 5 us to start (three walks, 10 us and
+// 15 us for the gradient), without outputs 1.9 us and 4 us (measured; T 8192, H 4,
+// d 128 forward: 164 us in one piece, 35 us in 16; B 4, T 4096, H 16: 94 us in one,
+// 146 us in two).  Of packed sequences the host does not know the lengths: those
+// longer than one and a half times an SM's share of all tokens are cut.
+int block_len(int n_seq, bool varlen, bool bwd, int T, int H, int ng, size_t nel) {
     const double sms = 148.0;
-    if (varlen) {
-        long L = (long)((double)T * H * ng / sms);
-        if (L < 512) L = 512;
-        if (L > T) L = T;
-        return (int)((L + kQ - 1) / kQ * kQ);
-    }
     const int ch = (T + kQ - 1) / kQ;
+    if (varlen) {
+        double L = 1.5 * T * H * ng / sms;
+        if (L < 256) L = 256;
+        if (L > T) L = T;
+        return ((int)L + kQ - 1) / kQ * kQ;
+    }
     int best = ch;
     double least = 1e30;
     for (int nb = 1; nb <= ch && nb <= 64; ++nb) {
         const int c = (ch + nb - 1) / nb;
-        if (nb > 1 && c < 4) break;
         auto waves = [&](double units) { return (double)(long)((units + sms - 1) / sms); };
-        double t = waves((double)n_seq * H * ng * nb) * (1.5 * c + 4);
+        const double walks = (double)n_seq * H * ng;
+        double t = waves(walks * nb) * (bwd ? 10.0 * c + 15 : 2.6 * c + 5);
         if (nb > 1)
-            t += waves((double)n_seq * H * ng * (nb - 1)) * (0.9 * c + 4) + 6 +
-                 (double)n_seq * nb * H * nel * 8 / 4e6;
+            t += (bwd ? 2 : 1) * (waves(walks * (nb - 1)) * (1.9 * c + 4) + 2 + 0.25 * nb +
+                                  (double)n_seq * nb * H * nel * 8 / 4e6);
         if (t < least * 0.97) {
             least = t;
             best = c;
@@ -1190,7 +1240,7 @@ TcWs tc_ws(const LinCall &c, bool bwd) {
     const int n_seq = varlen ? c.n_seq : c.B;
     const size_t nel = (size_t)c.dk_ * c.dv_, rows = (size_t)c.B * c.T;
     const int gk = groups(c.dk_), gv = groups(c.dv_);
-    w.L = block_len(n_seq, varlen, c.B, c.T, c.H, bwd && gk > gv ? gk : gv, nel);
+    w.L = block_len(n_seq, varlen, bwd, c.T, c.H, bwd && gk > gv ? gk : gv, nel);
     if (w.L < kQ) w.L = kQ;
     w.nb = (c.T + w.L - 1) / w.L;
     w.n_slots = varlen ? c.T / w.L + n_seq : c.B * w.nb;
@@ -1215,7 +1265,7 @@ TcWs tc_ws(const LinCall &c, bool bwd) {
         w.cp = take(rows * c.H * 2 * 4);
         w.dq32 = take(c.Hk < c.H ? rows * c.H * c.dk_ * 4 : 0);
         w.dk32 = take(c.Hk < c.H ? rows * c.H * c.dk_ * 4 : 0);
-        w.part = take((size_t)n_seq * c.H * 4);
+        w.part = take((size_t)kDgCtas * n_seq * c.H * 4);
     }
     w.total = o ? o : 256;  // 0 stands for a refused call
     return w;
@@ -1279,7 +1329,7 @@ cudaError_t lin_fwd_tc(const LinCall &c) {
     const TcWs w = tc_ws(c, false);
     const LinWs l = common_ws(w);
     Geo geo = lin_geo(c, l);
-    geo.keep_empty = 1;
+    geo.keep_empty = geo.skip_single = 1;
     const Plan plan = {(const int4 *)(c.ws + w.slot), (const int *)(c.ws + w.blk_start)};
     Maps m;
     if (!make_maps(&m, c)) return cudaErrorUnknown;
@@ -1297,8 +1347,8 @@ cudaError_t lin_fwd_tc(const LinCall &c) {
             return e;
         if ((e = lin_scan(c, geo, l, X, c.S0, nullptr, false)) != cudaSuccess) return e;
     }
-    p.multi = w.multi;
-    p.xin = w.multi ? X : c.S0;
+    p.xin = c.S0;
+    p.xblk = X;
     p.xout = c.S_final;
     p.out = c.out;
     return launch_chain<false, kOut>(c, geo, plan, m.q, m.k, m.v, p, GDR_K_LIN_OUT);
@@ -1308,7 +1358,7 @@ cudaError_t lin_bwd_tc(const LinCall &c) {
     const TcWs w = tc_ws(c, true);
     const LinWs l = common_ws(w);
     Geo geo = lin_geo(c, l);
-    geo.keep_empty = 1;
+    geo.keep_empty = geo.skip_single = 1;
     const Plan plan = {(const int4 *)(c.ws + w.slot), (const int *)(c.ws + w.blk_start)};
     Maps m;
     if (!make_maps(&m, c)) return cudaErrorUnknown;
@@ -1336,11 +1386,11 @@ cudaError_t lin_bwd_tc(const LinCall &c) {
     }
     // dq: (a, b, c) = (dout, v, k), the state transposed
     TcArgs p{};
-    p.multi = w.multi;
     p.ha = p.hb = c.H; p.hc = p.he = c.Hk;
     p.db = c.dv_; p.dc = c.dk_; p.tr = 1;
     p.out32 = shared;
-    p.xin = w.multi ? X : c.S0;
+    p.xin = c.S0;
+    p.xblk = X;
     p.xout = c.dS_final ? fin : nullptr;
     p.out = shared ? (void *)(c.ws + w.dq32) : c.dq;
     p.e = q;
@@ -1348,7 +1398,8 @@ cudaError_t lin_bwd_tc(const LinCall &c) {
     if ((e = launch_chain<false, kOutDots>(c, geo, plan, m.o, m.v, m.k, p, GDR_K_LIN_GRAD)) != cudaSuccess)
         return e;
     // dk: (v, dout, q), backward in time
-    p.xin = w.multi ? Y : c.dS_final;
+    p.xin = c.dS_final;
+    p.xblk = Y;
     p.xout = nullptr;
     p.out = shared ? (void *)(c.ws + w.dk32) : c.dk;
     p.e = k;
@@ -1357,10 +1408,10 @@ cudaError_t lin_bwd_tc(const LinCall &c) {
         return e;
     // dv: (k, q, dout), backward in time
     TcArgs r{};
-    r.multi = w.multi;
     r.ha = r.hb = c.Hk; r.hc = r.he = c.H;
     r.db = c.dk_; r.dc = c.dv_;
-    r.xin = w.multi ? Y : c.dS_final;
+    r.xin = c.dS_final;
+    r.xblk = Y;
     r.xout = c.dS0;
     r.out = c.dv;
     if ((e = launch_chain<true, kOut>(c, geo, plan, m.k, m.q, m.o, r, GDR_K_LIN_GRAD)) != cudaSuccess) return e;
@@ -1388,14 +1439,16 @@ cudaError_t lin_bwd_tc(const LinCall &c) {
         m.q, m.k, m.v, m.o, pa, geo, plan, c.err);
     prof_end(tk, c.st);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    DgArgs d{ri, ci, rp, cp, 2 * groups(c.dk_), 2 * groups(c.dk_), fin, c.dS_final, c.dg, part, c.dk_ * c.dv_};
+    const int rounds = (c.T + 8 * kQ - 1) / (8 * kQ), ctas = rounds < kDgCtas ? rounds : kDgCtas;
+    DgArgs d{ri, ci, rp, cp, 2 * groups(c.dk_), 2 * groups(c.dk_), fin, c.dS_final, c.dg, part, c.dk_ * c.dv_,
+             (rounds + ctas - 1) / ctas};
     tk = prof_begin(GDR_K_LIN_GRAD, c.st);
-    dg_chunks_kernel<<<(unsigned)(geo.n_seq * geo.H), 1024, 0, c.st>>>(d, c.cu, geo, plan);
+    dg_chunks_kernel<<<dim3((unsigned)(geo.n_seq * geo.H), (unsigned)ctas), 1024, 0, c.st>>>(d, c.cu, geo, plan);
     prof_end(tk, c.st);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (!part) return cudaSuccess;
     Geo by_seq = geo;  // one sum per sequence and head
-    by_seq.n_slots = geo.n_seq;
+    by_seq.n_slots = geo.n_seq * ctas;
     return lin_dg_heads(c, by_seq, part);
 }
 
