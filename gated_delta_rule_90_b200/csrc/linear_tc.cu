@@ -41,6 +41,7 @@ constexpr uint32_t kAtom = kQ * 128;     // bytes of 128 rows of 64 bf16
 constexpr float kLog2e = 1.4426950408889634f;
 
 enum { kStateOnly = 0, kOut = 1, kOutDots = 2 };
+constexpr int kRun = 4;  // chunks over which the gradient of the decays is summed before it starts again
 
 // Tables of a chunk's decays (floats): LC sums inside each 32-token block in
 // units of log 2, CF column factors, then scalars by block (see decay_tables).
@@ -89,6 +90,10 @@ struct TcArgs {
     void *out;           // bf16, or fp32 with out32
     const __nv_bfloat16 *e;  // dots: rows that the state's part of out is multiplied with
     float *dots;         // [2 x column groups, rows, H]
+    // dots, forward: the state where every kRun-th chunk of a block starts, as the state's threads
+    // hold it; reverse: its products with the gradient of that state, by warp
+    float *bnd, *ydot;
+    int nbnd;            // of a block
     int ha, hb, hc, he;  // heads of a, b, c, e
     int db, dc, ng;      // widths, column groups
     int tr;              // states are stored as the transpose of X
@@ -823,6 +828,40 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                     if (lane == 0) mbar_arrive(sdfree);
                 }
                 if (update && cc < nch && MODE != kStateOnly) {
+                    if (MODE == kOutDots) {
+                        const int e = nch - cc;  // reverse: the chunk whose start this is
+                        int at = -1;             // boundary: block, and start of the block's chunk at * kRun
+                        int bs = slot;
+                        if (!REV) {
+                            if (cc % kRun == 0) at = cc / kRun;
+                        } else if (cc > 0) {
+                            if (e % kRun == 0) at = e / kRun;
+                        } else if (sl.w < nblk - 1) {
+                            bs = slot + 1;
+                            at = 0;
+                        }
+                        if (at >= 0) {
+                            const size_t u = (((size_t)bs * p.nbnd + at) * geo.H + h) * p.ng + ng;
+                            float4 *b4 = reinterpret_cast<float4 *>(p.bnd) + u * (8 * 256) + (tid - 256);
+                            if (!REV) {
+#pragma unroll
+                                for (int v = 0; v < 8; ++v)
+                                    b4[v * 256] = make_float4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
+                            } else {
+                                float y = 0.f;
+                                if (k < p.db)
+#pragma unroll
+                                    for (int v = 0; v < 8; ++v) {
+                                        const float4 z = b4[v * 256];
+                                        y = fmaf(x[4 * v], z.x, fmaf(x[4 * v + 1], z.y,
+                                            fmaf(x[4 * v + 2], z.z, fmaf(x[4 * v + 3], z.w, y))));
+                                    }
+#pragma unroll
+                                for (int o = 16; o; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+                                if (lane == 0) p.ydot[u * 8 + (warp - 8)] = y;
+                            }
+                        }
+                    }
                     // X as the B operand of A X^T (row k, swizzled), once the last chunk's product is done
                     if (cc > 0) {
                         ok = ok && wait(ifull, (cc - 1) & 1, err);
@@ -1069,117 +1108,95 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 }
 
 // ------------------------------------------------------------ gradient of the decays
-// A CTA takes a run of chunks of a (sequence, head), from the last to the first, 8
-// at a time (128 threads each), in 64 bits:
-//     dg_t = sum_{l >= t in chunk} (R_l - C_l) + sum over later chunks (Ri - Ci) + <S_end, dS_end>,
+// A CTA takes a run of kRun chunks of a (block, head), in 64 bits:
+//     dg_t = sum_{l >= t in chunk} (R_l - C_l) + sum over the run's later chunks (Ri - Ci) + <S, dS>,
 // R = Ri + Rp, C = Ci + Cp: the state's part (dots of the chains) and the part of
 // the chunk's own pairs, whose rows and columns sum to the same and so drop out
-// of the carry.  S_end, dS_end at the end of the sequence.  Up to 16 CTAs share a
-// sequence; each sums the later chunks' part itself, all loads at once, which takes
-// less than waiting for the one before (T 8192, H 4: 32 us by one CTA, XX us).
+// of the carry; S, dS the state at the run's end and its gradient, whose product
+// the chains form at every kRun-th chunk.  Carried on from the end of the sequence
+// instead, the sum's error grew with the length (T 4096: 1.8e-6 to 6e-6 of dg).
+struct DgArgs {
+    const float *ri, *ci, *rp, *cp, *ydot;
+    int nri, nci, ny;           // planes of ri, ci; products of a boundary
+    const float *fin, *dfin;    // S, dS at the sequences' ends, or dfin NULL (zero)
+    float *dg, *part;
+    int nel, nbnd;
+};
 __device__ __forceinline__ double warp_sum(double x) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
 }
-constexpr int kDgCtas = 16;  // CTAs of a sequence and head at most
-struct DgArgs {
-    const float *ri, *ci, *rp, *cp;
-    int nri, nci;               // planes of ri, ci
-    const float *fin, *dfin;    // S_end, dS_end, or dfin NULL
-    float *dg, *part;
-    int nel, rounds;            // rounds of 8 chunks of a CTA
-};
 
-__global__ void __launch_bounds__(1024)
-dg_chunks_kernel(DgArgs p, const int32_t *__restrict__ cu, Geo geo, Plan plan) {
-    __shared__ double tot[32], inter[32], red[32];
-    const int s = blockIdx.x / geo.H, h = blockIdx.x - s * geo.H;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    long t0;
-    int len;
-    if (geo.varlen) {
-        const int a = plan.blk_start[s], b = plan.blk_start[s + 1];
-        t0 = plan.slot[a].x;
-        len = plan.slot[b - 1].x + plan.slot[b - 1].y - (int)t0;
-    } else {
-        t0 = (long)s * geo.T;
-        len = geo.T;
+__global__ void __launch_bounds__(kRun * kQ)
+dg_runs_kernel(DgArgs p, Geo geo, Plan plan) {
+    constexpr int NW = kRun * kQ / 32;
+    __shared__ double tot[NW], inter[NW], red[NW];
+    const int slot = blockIdx.x / geo.H, h = blockIdx.x - slot * geo.H, run = blockIdx.y;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, grp = tid / kQ;
+    const int4 sl = slot_of(geo, plan, slot);
+    const int first = run * kRun * kQ, len = sl.y - first;  // tokens from the run's start
+    if (len <= 0) {
+        if (p.part && tid == 0) p.part[((size_t)slot * p.nbnd + run) * geo.H + h] = 0.f;
+        return;
     }
+    const int nblk = geo.varlen ? plan.blk_start[sl.z + 1] - plan.blk_start[sl.z] : geo.nb;
+    const bool more = len > kRun * kQ;  // the block goes on after the run
     double f = 0.0;
-    if (p.dfin) {
-        const size_t o = (size_t)blockIdx.x * p.nel;
+    if (more || sl.w < nblk - 1) {
+        const size_t u = ((size_t)(more ? slot : slot + 1) * p.nbnd + (more ? run + 1 : 0)) * geo.H + h;
+        if (tid < p.ny) f = p.ydot[u * p.ny + tid];
+    } else if (p.dfin) {
+        const size_t o = ((size_t)sl.z * geo.H + h) * p.nel;
         float acc = 0.f;
-        for (int i = tid; i < p.nel / 4; i += 1024) {
+        for (int i = tid; i < p.nel / 4; i += kRun * kQ) {
             const float4 a = reinterpret_cast<const float4 *>(p.fin + o)[i];
             const float4 b = reinterpret_cast<const float4 *>(p.dfin + o)[i];
             acc = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, acc))));
         }
-        f = warp_sum((double)acc);
-        if (lane == 0) red[warp] = f;
-        __syncthreads();
-        f = warp_sum(red[lane]);
+        f = acc;
     }
-    const int nch = (len + kQ - 1) / kQ, grp = tid >> 7, j = tid & 127;
-    const int top = nch - 1 - 8 * p.rounds * (int)blockIdx.y, bottom = max(top - 8 * p.rounds, -1);
-    double all = 0.0, c0 = f;  // c0: the sum over the chunks behind
-    if (top < 0) {             // nothing left for this CTA
-        if (p.part && tid == 0) p.part[(size_t)blockIdx.y * gridDim.x + blockIdx.x] = 0.f;
+    double x = 0.0, y = 0.0;  // everything; the state's part
+    const size_t at = ((size_t)sl.x + first + tid) * geo.H + h, pl = (size_t)geo.rows * geo.H;
+    if (tid < len) {
+        for (int u = 0; u < p.nri; ++u) y += p.ri[u * pl + at];
+        for (int u = 0; u < p.nci; ++u) y -= p.ci[u * pl + at];
+        x = y + (((double)p.rp[at] + p.rp[pl + at]) - ((double)p.cp[at] + p.cp[pl + at]));
+    }
+    f = warp_sum(f);
+    const double ys = warp_sum(y);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {  // inclusive sum from the warp's end
+        const double z = __shfl_down_sync(0xffffffffu, x, o);
+        if (lane + o < 32) x += z;
+    }
+    if (lane == 0) {
+        tot[warp] = x;
+        inter[warp] = ys;
+        red[warp] = f;
+    }
+    __syncthreads();
+    // the boundary, the run's later chunks, and this chunk's later warps
+    constexpr int WC = kQ / 32;
+    double add = 0.0;
+    if (lane < NW) {
+        add = red[lane];
+        if (lane >= WC * (grp + 1)) add += inter[lane];
+        if (lane > warp && lane < WC * (grp + 1)) add += tot[lane];
+    }
+    x += warp_sum(add);
+    if (!p.part) {
+        if (tid < len) p.dg[at] = (float)x;
         return;
     }
-    if (blockIdx.y > 0) {
-        const size_t pl = (size_t)geo.rows * geo.H;
-        double y = 0.0;
-#pragma unroll 4
-        for (int i = (top + 1) * kQ + tid; i < len; i += 1024) {
-            const size_t at = ((size_t)t0 + i) * geo.H + h;
-            for (int u = 0; u < p.nri; ++u) y += p.ri[u * pl + at];
-            for (int u = 0; u < p.nci; ++u) y -= p.ci[u * pl + at];
-        }
-        y = warp_sum(y);
-        __syncthreads();
-        if (lane == 0) red[warp] = y;
-        __syncthreads();
-        c0 += warp_sum(red[lane]);
-    }
-    for (int base = top; base > bottom; base -= 8) {
-        const int cc = base - grp, i = cc * kQ + j;
-        double x = 0.0, y = 0.0;  // everything; the state's part
-        if (cc > bottom && i < len) {
-            const size_t at = ((size_t)t0 + i) * geo.H + h, pl = (size_t)geo.rows * geo.H;
-            for (int u = 0; u < p.nri; ++u) y += p.ri[u * pl + at];
-            for (int u = 0; u < p.nci; ++u) y -= p.ci[u * pl + at];
-            x = y + (((double)p.rp[at] + p.rp[pl + at]) - ((double)p.cp[at] + p.cp[pl + at]));
-        }
-        const double ys = warp_sum(y);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {  // inclusive sum from the warp's end
-            const double z = __shfl_down_sync(0xffffffffu, x, o);
-            if (lane + o < 32) x += z;
-        }
-        __syncthreads();  // the last round's readers are done
-        if (lane == 0) {
-            tot[warp] = x;
-            inter[warp] = ys;
-        }
-        __syncthreads();
-        // the chunks behind this one, and this chunk's warps behind
-        x += c0 + warp_sum((lane < 4 * grp ? inter[lane] : 0.0) + (lane > warp && lane < 4 * grp + 4 ? tot[lane] : 0.0));
-        c0 += warp_sum(inter[lane]);
-        if (cc > bottom && i < len) {
-            if (p.part)
-                all += x;
-            else
-                p.dg[((size_t)t0 + i) * geo.H + h] = (float)x;
-        }
-    }
-    if (!p.part) return;
-    all = warp_sum(all);
     __syncthreads();
-    if (lane == 0) red[warp] = all;
+    x = warp_sum(tid < len ? x : 0.0);
+    if (lane == 0) red[warp] = x;
     __syncthreads();
-    all = warp_sum(red[lane]);
-    if (tid == 0) p.part[(size_t)blockIdx.y * gridDim.x + blockIdx.x] = (float)all;
+    if (warp == 0) {
+        x = warp_sum(lane < NW ? red[lane] : 0.0);
+        if (lane == 0) p.part[((size_t)slot * p.nbnd + run) * geo.H + h] = (float)x;
+    }
 }
 
 }  // namespace lin
@@ -1231,8 +1248,8 @@ int block_len(int n_seq, bool varlen, bool bwd, int T, int H, int ng, size_t nel
 }
 
 struct TcWs {
-    size_t slot, blk_start, gtot, X, Y, fin, ri, ci, rp, cp, dq32, dk32, part, total;
-    int L, nb, n_slots, multi;
+    size_t slot, blk_start, gtot, X, Y, fin, ri, ci, rp, cp, bnd, ydot, dq32, dk32, part, total;
+    int L, nb, n_slots, multi, nbnd;
 };
 TcWs tc_ws(const LinCall &c, bool bwd) {
     TcWs w{};
@@ -1245,6 +1262,7 @@ TcWs tc_ws(const LinCall &c, bool bwd) {
     w.nb = (c.T + w.L - 1) / w.L;
     w.n_slots = varlen ? c.T / w.L + n_seq : c.B * w.nb;
     w.multi = w.nb > 1;
+    w.nbnd = (w.L + kRun * kQ - 1) / (kRun * kQ);
     const size_t sh = (size_t)w.n_slots * c.H;
     size_t o = 0;
     auto take = [&](size_t bytes) {
@@ -1265,7 +1283,9 @@ TcWs tc_ws(const LinCall &c, bool bwd) {
         w.cp = take(rows * c.H * 2 * 4);
         w.dq32 = take(c.Hk < c.H ? rows * c.H * c.dk_ * 4 : 0);
         w.dk32 = take(c.Hk < c.H ? rows * c.H * c.dk_ * 4 : 0);
-        w.part = take((size_t)kDgCtas * n_seq * c.H * 4);
+        w.bnd = take(sh * w.nbnd * gk * kN * 128 * 4);
+        w.ydot = take(sh * w.nbnd * gk * 8 * 4);
+        w.part = take(sh * w.nbnd * 4);
     }
     w.total = o ? o : 256;  // 0 stands for a refused call
     return w;
@@ -1395,6 +1415,9 @@ cudaError_t lin_bwd_tc(const LinCall &c) {
     p.out = shared ? (void *)(c.ws + w.dq32) : c.dq;
     p.e = q;
     p.dots = ri;
+    p.bnd = (float *)(c.ws + w.bnd);
+    p.ydot = (float *)(c.ws + w.ydot);
+    p.nbnd = w.nbnd;
     if ((e = launch_chain<false, kOutDots>(c, geo, plan, m.o, m.v, m.k, p, GDR_K_LIN_GRAD)) != cudaSuccess)
         return e;
     // dk: (v, dout, q), backward in time
@@ -1439,17 +1462,16 @@ cudaError_t lin_bwd_tc(const LinCall &c) {
         m.q, m.k, m.v, m.o, pa, geo, plan, c.err);
     prof_end(tk, c.st);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    const int rounds = (c.T + 8 * kQ - 1) / (8 * kQ), ctas = rounds < kDgCtas ? rounds : kDgCtas;
-    DgArgs d{ri, ci, rp, cp, 2 * groups(c.dk_), 2 * groups(c.dk_), fin, c.dS_final, c.dg, part, c.dk_ * c.dv_,
-             (rounds + ctas - 1) / ctas};
+    DgArgs d{ri, ci, rp, cp, (const float *)(c.ws + w.ydot), 2 * groups(c.dk_), 2 * groups(c.dk_),
+             8 * groups(c.dk_), fin, c.dS_final, c.dg, part, c.dk_ * c.dv_, w.nbnd};
     tk = prof_begin(GDR_K_LIN_GRAD, c.st);
-    dg_chunks_kernel<<<dim3((unsigned)(geo.n_seq * geo.H), (unsigned)ctas), 1024, 0, c.st>>>(d, c.cu, geo, plan);
+    dg_runs_kernel<<<dim3((unsigned)units, (unsigned)w.nbnd), kRun * kQ, 0, c.st>>>(d, geo, plan);
     prof_end(tk, c.st);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (!part) return cudaSuccess;
-    Geo by_seq = geo;  // one sum per sequence and head
-    by_seq.n_slots = geo.n_seq * ctas;
-    return lin_dg_heads(c, by_seq, part);
+    Geo by_run = geo;  // one sum per run and head
+    by_run.n_slots = geo.n_slots * w.nbnd;
+    return lin_dg_heads(c, by_run, part);
 }
 
 }  // namespace gdr_host
