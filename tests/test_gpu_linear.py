@@ -260,6 +260,64 @@ def test_streams_and_graphs(cuda_device, path, dtype):
         assert all(torch.equal(p, q) for p, q in zip(w[1], b))
 
 
+# one sequence long enough to be cut into blocks; a packed batch with an empty sequence, one token, and long ones
+LONG = [(2500, 1, 1, 128, 128, "token", None), (2500, 2, 1, 64, 112, "head", None),
+        (2600, 2, 1, 128, 48, "token", [0, 0, 1500, 1501, 2600]), (1800, 1, 1, 80, 128, "head", [0, 1537, 1800, 1800])]
+
+
+@pytest.mark.parametrize("path,dtype", PATHS)
+@pytest.mark.parametrize("T,H,Hk,dk,dv,gate,cu", LONG)
+def test_long_sequences(cuda_device, path, dtype, T, H, Hk, dk, dv, gate, cu):
+    x = inputs(cuda_device, 14, 1, T, H, Hk, dk, dv, dtype, gate, cu)
+    out, S = fwd(x, path=path)
+    r, Sr = ref.forward(*d64(x["q"], x["k"], x["v"], x["g"], x["S0"]), cu=cu)
+    assert rel(out, r) <= tol_out(dtype, path) and rel(S, Sr) <= TOL32
+    got = bwd(x, path=path)
+    want = ref.gradients(*d64(x["q"], x["k"], x["v"], x["g"], x["dout"], x["S0"], x["dS"]), cu=cu)
+    for name, a, b in zip(("dq", "dk", "dv", "dg", "dS0"), got, want):
+        tol = tol_out(dtype, path) if name in ("dq", "dk", "dv") else 2 * TOL32
+        assert rel(a, b) <= tol, (name, rel(a, b))
+
+
+@pytest.mark.parametrize("path,dtype", PATHS)
+def test_outputs_at_16_byte_offsets(cuda_device, path, dtype):
+    """Output and input views that start 16 bytes into their storage give the same bits."""
+    x = inputs(cuda_device, 15, 1, 150, 2, 2, 48, 80, dtype)
+
+    def shifted(t):
+        n = 16 // t.element_size()
+        v = torch.empty(t.numel() + n, dtype=t.dtype, device=t.device)[n:].view(t.shape)
+        v.copy_(t)
+        return v
+
+    y = {k: (shifted(t) if torch.is_tensor(t) else t) for k, t in x.items()}
+    out, S = fwd(x, path=path)
+    o2, S2 = fwd(y, path=path, out=shifted(out), S_final=shifted(S))
+    assert torch.equal(out, o2) and torch.equal(S, S2)
+    a = bwd(x, path=path)
+    b = bwd(y, path=path, **{n: shifted(t) for n, t in zip(("dq", "dk", "dv", "dg", "dS0"), a)})
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_gradient_against_differences(cuda_device):
+    """The fp32 gradients against central differences of the fp32 forward along one direction: step 2^-6,
+    error O(step^2) of third derivatives of size about 1, and 2 sums of n terms rounded at 2^-24 over the step."""
+    x = inputs(cuda_device, 16, 1, 40, 2, 1, 32, 16, F32, scale=0.3)
+    got = dict(zip(("q", "k", "v", "g", "S0"), bwd(x)))
+    gen = torch.Generator(device=cuda_device).manual_seed(17)
+    for name, d in got.items():
+        u = torch.randn(x[name].shape, generator=gen, device=cuda_device)
+        u /= u.norm()
+        loss = []
+        for sign in (1, -1):
+            y = dict(x)
+            y[name] = x[name] + sign * 2.0 ** -6 * u
+            out, S = fwd(y)
+            loss.append(float((out.double() * x["dout"].double()).sum() + (S.double() * x["dS"].double()).sum()))
+        slope, want = (loss[0] - loss[1]) * 2.0 ** 5, float((d.double() * u.double()).sum())
+        assert abs(slope - want) <= 1e-3 * float(d.norm()), name
+
+
 def test_empty_calls(cuda_device):
     """No tokens: S_final is S0 (or zero), dS0 is dS_final."""
     dev = cuda_device
