@@ -419,7 +419,7 @@ def _linear_args(q, k, v, g, tensors):
     for name, t in (("v", v), ("g", g)):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
-    dev, qs, vs, tok = q.device, q.shape, v.shape, q.dtype
+    dev, at, qs, vs, tok = q.device, q.get_device(), q.shape, v.shape, q.dtype
     *lead, H_k, d_k = qs
     H, d_v = vs[-2:]
     gate = GDR_GATE_HEAD if g.dim() == 1 else GDR_GATE_SCALAR
@@ -432,7 +432,7 @@ def _linear_args(q, k, v, g, tensors):
                  ("g", g, torch.float32, (H,) if gate else (*lead, H)), *tensors):
         t = spec[1]
         if t is not None and not (isinstance(t, torch.Tensor) and t.shape == spec[3] and
-                                  t.dtype == spec[2] and t.is_contiguous() and t.device == dev):
+                                  t.dtype is spec[2] and t.is_contiguous() and t.get_device() == at):
             _linear_bad(dev, *spec)
     return dev, _dtype_code(q), gate, H, H_k, d_k, d_v
 
@@ -525,7 +525,10 @@ def gdr_decode_step_linear(q, k, v, g, S, *, out=None, stream=None) -> torch.Ten
             q.data_ptr(), _addr(k), v.data_ptr(), g.data_ptr(), _addr(S), o.data_ptr(), N, H,
             H_k, d_k, d_v, dtype, gate, handle)
 
-    out, st = _linear_call(dev, stream, 0, None, call)
+    if stream is None and torch.cuda.current_device() == dev.index:
+        out, st = call(0, 0, torch._C._cuda_getCurrentRawStream(dev.index))
+    else:
+        out, st = _linear_call(dev, stream, 0, None, call)
     if st != GDR_OK:
         raise GdrError(st, "gdr_decode_step_linear")
     return out

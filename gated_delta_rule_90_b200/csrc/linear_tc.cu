@@ -219,9 +219,8 @@ __device__ __forceinline__ float load_raw_g(const Geo &geo, const float *g, long
 
 // A number in two floats, hi + lo (about 48 bits): sums by Knuth's exact two-sum.
 // The running sums of log-decays need it, for differences of far positions have to
-// be rounded once, not at the size of the sums.  In fp64 the sums took 6 times as
-// long: its units gave an addition every few hundred cycles beside the tensor
-// cores' work (forward, B4 T4096 H16 d128: 109 us, 90 so).
+// be rounded once, not at the size of the sums.  In fp64 the
+// chunks waited for them (forward, B4 T4096 H16 d128: 106 us, 99 so).
 struct Two {
     float h, l;
 };
@@ -302,9 +301,8 @@ __device__ __forceinline__ float row_factor(const float *tab, int rb, float li) 
     return exp2f(REV ? tab[kLE + rb] - li : li);
 }
 
-// Roles of the 21 warps: 8 of outputs, 8 of the state; TMA, decays, and the MMAs
-// of P, of A X^T and P C, and of (w C)^T B.  One thread gets an MMA through about
-// every 105 cycles whatever its width, so three issue.  Each role works a chunk
+// Roles of the 20 warps: 8 of outputs, 8 of the state; the decays; TMA with the MMAs
+// of P; the MMAs of A X^T and P C; those of (w C)^T B.  Each role works a chunk
 // ahead of the one that needs its results, over mbarriers; no wait lags a barrier
 // by two phases (every phase needs an arrival of the waiter, or of one that
 // follows it).
@@ -391,7 +389,7 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     auto chunk_at = [&](int cc) { return (REV ? nch - 1 - cc : cc) * kQ; };
 
     if (warp == 16) {
-        // ===================== TMA loads and decays =====================
+        // ===================== decays =====================
         float gv[4];
         auto load = [&](int cc) {
             const int j0 = chunk_at(cc), n = min(kQ, len - j0);
@@ -400,9 +398,30 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                 gv[u] = 4 * lane + u < n ? load_raw_g(geo, p.g, (long)t0 + j0 + 4 * lane + u, h) : 0.f;
         };
         Two tot = {0.f, 0.f};
-        // the tiles of chunk cc, as their buffers fall free.  (The whole warp waits: with the waits
-        // under a branch on the lane, the code after it ran apart for that lane, and the decays
-        // took five times as long.)
+        if (nch > 0) load(0);
+        for (int cc = 0; cc < nch; ++cc) {
+            const int i2 = cc & 1;
+            if (cc >= 2) ok = ok && wait(&tfree[i2], (cc / 2 - 1) & 1, err);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) gv[u] = clamp_g(gv[u]);
+            tot = add(tot, decay_tables<REV>(tabs + i2 * kTab, gv, lane));
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&fullC[i2]);
+                if (MODE != kStateOnly) mbar_arrive(&pfull[i2]);
+            }
+            __syncwarp();
+            if (cc + 1 < nch) load(cc + 1);
+        }
+        if (MODE == kStateOnly && p.gtot && ng == 0) {
+            if (lane == 0) p.gtot[(size_t)slot * geo.H + h] = tot.h;
+        }
+    } else if (warp == 17) {
+        // ===================== TMA loads; MMA: P = A B^T =====================
+        // the tiles of chunk cc, as their buffers fall free.  (The whole warp waits: under a branch
+        // on the lane, the code after the waits ran apart for that lane and took several times as long.)
         auto issue = [&](int cc) {
             const int i2 = cc & 1, y = t0 + chunk_at(cc), ia = SM::NA == 2 ? i2 : 0;
             if (cc >= 2) ok = ok && wait(&freeB[i2], (cc / 2 - 1) & 1, err);
@@ -428,48 +447,15 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                 __syncwarp();
             }
         };
-        if (nch > 0) {
-            load(0);
-            issue(0);
-        }
+        const uint32_t el = elect_lane(), idP = idesc_bf16(128, 128, 0, 0);
+        const uint64_t dA = sdesc_sw128(smem_u32(sm + SM::A), 16, 1024);
+        const uint64_t dB = sdesc_sw128(smem_u32(sm + SM::B), 16, 1024);
+        const int ks = p.db / 16;
+        // ahead of the products as far as the buffers go
+#pragma unroll 1
+        for (int cc = 0; cc < min(nch, SM::NA); ++cc) issue(cc);
         for (int cc = 0; cc < nch; ++cc) {
-            // the decays of chunk cc before its tiles: their buffer is free earlier
-            const int i2 = cc & 1;
-            if (cc >= 2) ok = ok && wait(&tfree[i2], (cc / 2 - 1) & 1, err);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) gv[u] = clamp_g(gv[u]);
-            tot = add(tot, decay_tables<REV>(tabs + i2 * kTab, gv, lane));
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&fullC[i2]);
-                if (MODE != kStateOnly) mbar_arrive(&pfull[i2]);
-            }
-            __syncwarp();
-            if (cc + 1 < nch) load(cc + 1);
-            if (cc > 0) issue(cc);
-        }
-        if (MODE == kStateOnly && p.gtot && ng == 0) {
-            if (lane == 0) p.gtot[(size_t)slot * geo.H + h] = tot.h;
-        }
-        // every load has landed and every product has read its tiles before the CTA ends:
-        // free(i) follows full(i), so waiting for the last use of each buffer covers both
-        for (int cc = max(nch - 2, 0); cc < nch; ++cc) {
-            wait(&freeB[cc & 1], (cc / 2) & 1, err);
-            wait(&freeC[cc & 1], (cc / 2) & 1, err);
-            if (MODE != kStateOnly && cc >= nch - SM::NA)
-                wait(&freeA[SM::NA == 2 ? cc & 1 : 0], (cc / SM::NA) & 1, err);
-        }
-        __syncwarp();
-    } else if (warp == 17) {
-        // ===================== MMA: P = A B^T =====================
-        if (MODE != kStateOnly) {
-            const uint32_t el = elect_lane(), idP = idesc_bf16(128, 128, 0, 0);
-            const uint64_t dA = sdesc_sw128(smem_u32(sm + SM::A), 16, 1024);
-            const uint64_t dB = sdesc_sw128(smem_u32(sm + SM::B), 16, 1024);
-            const int ks = p.db / 16;
-            for (int cc = 0; cc < nch; ++cc) {
+            if (MODE != kStateOnly) {
                 const int i2 = cc & 1, ia = SM::NA == 2 ? i2 : 0;
                 ok = ok && wait(&fullA[ia], (cc / SM::NA) & 1, err);
                 ok = ok && wait(&fullB[i2], (cc >> 1) & 1, err);
@@ -480,17 +466,28 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t da = sdesc_add(dA, ia * 2 * kAtom), db = sdesc_add(dB, i2 * 2 * kAtom);
-#pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    if (kk < ks) {
-                        const uint32_t o = (kk >> 2) * kAtom + (kk & 3) * 32;
-                        mma_ss(el, tmem + TM::P, sdesc_add(da, o), sdesc_add(db, o), idP, kk > 0);
-                    }
+#pragma unroll 1
+                for (int kk = 0; kk < ks; ++kk) {
+                    const uint32_t o = (kk >> 2) * kAtom + (kk & 3) * 32;
+                    mma_ss(el, tmem + TM::P, sdesc_add(da, o), sdesc_add(db, o), idP, kk > 0);
+                }
                 commit(el, &freeA[ia]);
                 commit(el, &freeB[i2]);
                 commit(el, &pfull[i2]);
             }
+            if (cc + 1 >= SM::NA && cc + 1 < nch) issue(cc + 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
         }
+        // every load has landed and every product has read its tiles before the CTA ends:
+        // free(i) follows full(i), so waiting for the last use of each buffer covers both
+        for (int cc = max(nch - 2, 0); cc < nch; ++cc) {
+            wait(&freeB[cc & 1], (cc / 2) & 1, err);
+            wait(&freeC[cc & 1], (cc / 2) & 1, err);
+            if (MODE != kStateOnly && cc >= nch - SM::NA)
+                wait(&freeA[SM::NA == 2 ? cc & 1 : 0], (cc / SM::NA) & 1, err);
+        }
+        __syncwarp();
     } else if (warp == 18) {
         // ===================== MMA: OIN = A X^T, O = P C =====================
         if (MODE != kStateOnly) {
@@ -513,7 +510,7 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                         tc_fence_after();
                         const uint64_t d = sdesc_add(dC, i2 * kAtom);
                         const uint32_t tO = tmem + TM::O + (TM::LAG ? i2 * kN : 0);
-#pragma unroll
+#pragma unroll 1
                         for (int kk = 0; kk < 8; ++kk)
                             mma_ts(el, tO, tmem + TM::P + kk * 16, sdesc_add(d, kk * 2048), idN, kk > 0);
                         commit(el, &freeC[i2]);
@@ -526,17 +523,16 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                         if (!ok) break;
                         tc_fence_after();
                         const uint64_t da = sdesc_add(dA, ia * 2 * kAtom);
-#pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            if (kk < ks) {
-                                const uint64_t a = sdesc_add(da, (kk >> 2) * kAtom + (kk & 3) * 32);
-                                const uint64_t b = sdesc_add(dX, kk * 2048);
-                                mma_ss(el, tmem + TM::OIN, a, b, idN, kk > 0);
-                                if (TM::DOTS) {
-                                    mma_ss(el, tmem + TM::OIN + kN, a, sdesc_add(b, kAtom), idN, kk > 0);
-                                    mma_ss(el, tmem + TM::OIN + kN, a, sdesc_add(b, 2 * kAtom), idN, 1);
-                                }
+#pragma unroll 1
+                        for (int kk = 0; kk < ks; ++kk) {
+                            const uint64_t a = sdesc_add(da, (kk >> 2) * kAtom + (kk & 3) * 32);
+                            const uint64_t b = sdesc_add(dX, kk * 2048);
+                            mma_ss(el, tmem + TM::OIN, a, b, idN, kk > 0);
+                            if (TM::DOTS) {
+                                mma_ss(el, tmem + TM::OIN + kN, a, sdesc_add(b, kAtom), idN, kk > 0);
+                                mma_ss(el, tmem + TM::OIN + kN, a, sdesc_add(b, 2 * kAtom), idN, 1);
                             }
+                        }
                         commit(el, &freeA[ia]);
                         commit(el, ifull);
                     }
@@ -556,13 +552,13 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                 ok = ok && wait(&fullB[i2], (cc >> 1) & 1, err);
                 if (cc > 0) ok = ok && wait(sdfree, (cc - 1) & 1, err);
                 const uint64_t db = sdesc_add(dB, i2 * 2 * kAtom);
-#pragma unroll
+#pragma unroll 1
                 for (int hf = 0; hf < 2; ++hf) {
                     ok = ok && wait(&cready[hf], cc & 1, err);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                     for (int kk = 4 * hf; kk < 4 * hf + 4; ++kk)
                         mma_ss(el, tmem + TM::SD, sdesc_add(db, kk * 2048), sdesc_add(dP, kk * 2048), idS, kk > 0);
                     if (hf == 0) commit(el, sfree);
