@@ -119,7 +119,7 @@ scan_kernel(float *__restrict__ X, const float *__restrict__ gtot, const float *
 
 // ------------------------------------------------------------ sums
 // The gradient of a shared query/key head: the sum over its value heads, fp32.
-// A CTA takes 16 tokens of a slot.
+// A CTA takes 16 tokens of a slot at a time.
 constexpr int kSumRows = 16;
 template <typename T>
 __global__ void __launch_bounds__(256)
@@ -127,8 +127,8 @@ group_sum_kernel(const float *__restrict__ x, T *__restrict__ out, Geo geo, Plan
     // slot by slot, so that rows of no sequence are left as they are
     const int4 sl = slot_of(geo, plan, blockIdx.x);
     const int r = geo.H / geo.Hk, per = geo.Hk * (d / 4);
-    const int j0 = blockIdx.y * kSumRows, n = min(kSumRows, sl.y - j0);
-    for (int i = threadIdx.x; i < n * per; i += 256) {
+    for (int j0 = blockIdx.y * kSumRows; j0 < sl.y; j0 += gridDim.y * kSumRows)
+    for (int i = threadIdx.x; i < min(kSumRows, sl.y - j0) * per; i += 256) {
         const long row = sl.x + j0 + i / per;
         const int hk = (i % per) / (d / 4), d4 = (i % per) % (d / 4);
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -264,8 +264,8 @@ gdr_status check_shapes(int B, int T, int H, int Hk, int dk, int dv, int n_seq, 
     const gdr_status st = check_types(H, Hk, dk, dv, dtype, gate);
     if (st != GDR_OK) return st;
     const double n = varlen ? n_seq : B;
-    // rows, slots and (sequence, head) pairs are counted in 32 bits
-    if ((double)B * T > 2.0e9 || n * H > 2.0e9 || ((double)B * T / 128 + n) > 2.0e9)
+    // rows, and walks (blocks of at least 128 tokens, heads, two column groups), are counted in 32 bits
+    if ((double)B * T > 2.0e9 || n * H > 2.0e9 || ((double)B * T / 128 + n) * H * 2 > 2.1e9)
         return GDR_ERR_INVALID;
     return GDR_OK;
 }
@@ -374,7 +374,8 @@ cudaError_t lin_group_sum(const LinCall &c, const Geo &geo, const LinWs &w, cons
                           int d) {
     if (!geo.n_slots) return cudaSuccess;
     const Plan plan = {(const int4 *)(c.ws + w.slot), (const int *)(c.ws + w.blk_start)};
-    const dim3 grid(geo.n_slots, (geo.L + kSumRows - 1) / kSumRows);
+    const int rounds = (geo.L + kSumRows - 1) / kSumRows;
+    const dim3 grid(geo.n_slots, rounds < 4096 ? rounds : 4096);
     ProfToken tk = prof_begin(GDR_K_LIN_SUM, c.st);
     if (c.dtype == GDR_BF16)
         group_sum_kernel<__nv_bfloat16><<<grid, 256, 0, c.st>>>(x, (__nv_bfloat16 *)out, geo,

@@ -385,7 +385,7 @@ Plan plan_of(const gdr_host::LinCall &c, const gdr_host::LinWs &w) {
 
 gdr_host::LinWs simt_ws(const gdr_host::LinCall &c, bool bwd) {
     // Blocks of up to 256 tokens; of fewer, down to one chunk, while the grid would leave SMs idle:
-    // a block's chunks run one after another (T 100, H 4, d 64: XX us of 256, XX us of 32)
+    // a block's chunks run one after another (gradients of T 100, H 4, d 64: 107 us in blocks of 256, 55 us of 32)
     int L = kBlk;
     while (L > kC) {
         const double slots = c.cu ? (double)c.T / L + c.n_seq : (double)c.B * ((c.T + L - 1) / L);

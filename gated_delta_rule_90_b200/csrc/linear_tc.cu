@@ -14,7 +14,9 @@
 // head for 64 columns of c; A, B, C tiles come by TMA, all products run on
 // tcgen05 with accumulators in tensor memory, and the carried state stays in
 // registers, fp32.  The state's own chain is one multiply-add per element and
-// chunk: (w C)^T B does not depend on X, so the chunks' products overlap.
+// chunk: (w C)^T B does not depend on X, so the chunks' products overlap.  64
+// columns, not all of d_c: two walks of a head then share a and b through L2, and
+// shared memory holds two buffers of each tile beside the split.
 //
 // Precision.  bf16 operands are exact in every product of two inputs.  P is
 // rounded to bf16 once (it multiplies C) and so is X where it multiplies A for
@@ -309,7 +311,9 @@ __device__ __forceinline__ float row_factor(const float *tab, int rb, float li) 
 //
 // Loops over columns are rolled where they can be: the five roles' unrolled code
 // did not fit the instruction caches, and warps waited for instructions most of
-// the time (forward, B4 T4096 H16 d128: 225 us unrolled, 105 us rolled).
+// the time (forward, B4 T4096 H16 d128: 225 us unrolled, 151 us rolled; 93 us now).
+// Bound by the latencies of the chain of hand-offs of a chunk (5,500 cycles), not by
+// a pipe: issue slots 52 %, tensor 35 %, shared memory 46 %, DRAM 31 % busy at that size.
 template <bool REV, int MODE>
 __global__ void __launch_bounds__(kTcThreads, 1)
 chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
@@ -913,7 +917,8 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
 // q_l . dq_l) and column sums (of k_m . dk_m), fp32.  Both factors are products
 // of inputs, so no operand is rounded.  The column sums are the row sums of the
 // transposed products, which the tensor cores form as well: 32 more MMAs cost
-// less than summing over lanes.  Reads q, k, v, dout once: HBM-bound.
+// less than summing over lanes.  Reads q, k, v, dout once.  B4 T4096 H16 d128: 69 us
+// (its bytes 41 us), with 8 warps for the sums 125.
 struct PairArgs {
     const float *g;
     float *rsum, *csum;  // [2, rows, H]
@@ -1425,15 +1430,6 @@ cudaError_t lin_bwd_tc(const LinCall &c) {
     p.dots = ci;
     if ((e = launch_chain<true, kOutDots>(c, geo, plan, m.v, m.o, m.q, p, GDR_K_LIN_GRAD)) != cudaSuccess)
         return e;
-    // dv: (k, q, dout), backward in time
-    TcArgs r{};
-    r.ha = r.hb = c.Hk; r.hc = r.he = c.H;
-    r.db = c.dk_; r.dc = c.dv_;
-    r.xin = c.dS_final;
-    r.xblk = Y;
-    r.xout = c.dS0;
-    r.out = c.dv;
-    if ((e = launch_chain<true, kOut>(c, geo, plan, m.k, m.q, m.o, r, GDR_K_LIN_GRAD)) != cudaSuccess) return e;
     if (shared) {
         if ((e = lin_group_sum(c, geo, l, (const float *)(c.ws + w.dq32), c.dq, c.dk_)) != cudaSuccess) return e;
         if ((e = lin_group_sum(c, geo, l, (const float *)(c.ws + w.dk32), c.dk, c.dk_)) != cudaSuccess) return e;
@@ -1464,10 +1460,20 @@ cudaError_t lin_bwd_tc(const LinCall &c) {
     dg_runs_kernel<<<dim3((unsigned)units, (unsigned)w.nbnd), kRun * kQ, 0, c.st>>>(d, geo, plan);
     prof_end(tk, c.st);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if (!part) return cudaSuccess;
-    Geo by_run = geo;  // one sum per run and head
-    by_run.n_slots = geo.n_slots * w.nbnd;
-    return lin_dg_heads(c, by_run, part);
+    if (part) {
+        Geo by_run = geo;  // one sum per run and head
+        by_run.n_slots = geo.n_slots * w.nbnd;
+        if ((e = lin_dg_heads(c, by_run, part)) != cudaSuccess) return e;
+    }
+    // dv: (k, q, dout), backward in time; last, since dS0 may be written over dS_final
+    TcArgs r{};
+    r.ha = r.hb = c.Hk; r.hc = r.he = c.H;
+    r.db = c.dk_; r.dc = c.dv_;
+    r.xin = c.dS_final;
+    r.xblk = Y;
+    r.xout = c.dS0;
+    r.out = c.dv;
+    return launch_chain<true, kOut>(c, geo, plan, m.k, m.q, m.o, r, GDR_K_LIN_GRAD);
 }
 
 }  // namespace gdr_host

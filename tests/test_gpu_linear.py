@@ -318,6 +318,17 @@ def test_gradient_against_differences(cuda_device):
         assert abs(slope - want) <= 1e-3 * float(d.norm()), name
 
 
+@pytest.mark.parametrize("path,dtype", PATHS)
+@pytest.mark.parametrize("T", [70, 1300])
+def test_state_gradient_in_place(cuda_device, path, dtype, T):
+    """dS0 written over dS_final: the same results."""
+    x = inputs(cuda_device, 18, 1, T, 2, 1, 64, 48, dtype, "head")
+    a = bwd(x, path=path)
+    y = dict(x, dS=x["dS"].clone())
+    b = bwd(y, path=path, dS0=y["dS"])
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
 def test_empty_calls(cuda_device):
     """No tokens: S_final is S0 (or zero), dS0 is dS_final."""
     dev = cuda_device
