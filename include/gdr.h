@@ -297,9 +297,11 @@ gdr_status gdr_fwd_frame(const void *q, const void *k, const void *v, const floa
  *           workspace: as for gdr_fwd.  Offsets that decrease or leave [0, T]
  *           are taken as their running maximum inside [0, T]; rows that belong
  *           to no sequence are not written.
- *  d_k, d_v multiples of 16 in [16, 128].  The tensor-core path takes bf16;
- *           fp32 tokens run on the CUDA cores.  S_final keeps fp32 accuracy
- *           on either path.
+ *  d_k, d_v multiples of 16 in [16, 128].  The tensor-core path takes bf16
+ *           (GDR_PATH_AUTO: every bf16 call with tokens); fp32 tokens run on the
+ *           CUDA cores.  S_final keeps fp32 accuracy on either path; a bf16 out
+ *           of the tensor-core path also rounds the weights of a chunk's pairs
+ *           and the state it reads to bf16, once each.  S_final may be S0.
  * gdr_decode_step_linear: one token per sequence, in place on S_inout.
  *  q, k [N, H_k, d_k]; v, out [N, H, d_v]; g [N, H] or [H]; S_inout
  *  [N, H, d_v, d_k]; the same d_k, d_v.
@@ -310,8 +312,8 @@ gdr_status gdr_fwd_frame(const void *q, const void *k, const void *v, const floa
  *           share a query/key head, then rounded once); dv [B, T, H, d_v] dtype
  *  dg       as g, fp32 (GDR_GATE_HEAD: summed over all tokens)
  *  dS0      [N, H, d_v, d_k]  fp32, gradient of S0, or NULL to skip
- *  dg and dS0 keep fp32 accuracy on either path.  No atomics: results do not
- *  change from run to run.
+ *  dg and dS0 keep fp32 accuracy on either path; dS0 may be dS_final.  No
+ *  atomics: results do not change from run to run.
  * The *_workspace_size functions return the bytes of device workspace (256-byte
  * aligned), 0 for arguments the call would reject.
  */
