@@ -38,7 +38,6 @@ constexpr int kQ = 128;                  // tokens of a chunk
 constexpr int kN = 64;                   // columns of c of a CTA
 constexpr uint32_t kSpinTc = 1u << 24;   // poll limit of every mbarrier wait
 constexpr int kTcThreads = 640;          // 8 output warps, 8 state warps, TMA and decays, 3 MMA issuers
-constexpr int kPairThreads = 640;        // TMA, MMA, decays of rows and columns; 8 warps each for their sums
 constexpr uint32_t kAtom = kQ * 128;     // bytes of 128 rows of 64 bf16
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -315,10 +314,9 @@ __device__ __forceinline__ float row_factor(const float *tab, int rb, float li) 
 // Bound by the latencies of the chain of hand-offs of a chunk (5,500 cycles), not by
 // a pipe: issue slots 52 %, tensor 35 %, shared memory 46 %, DRAM 31 % busy at that size.
 template <bool REV, int MODE>
-__global__ void __launch_bounds__(kTcThreads, 1)
-chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-             const __grid_constant__ CUtensorMap tm_c, TcArgs p, Geo geo, Plan plan,
-             unsigned int *err) {
+__device__ __forceinline__ void walk(unsigned int bid, const CUtensorMap &tm_a, const CUtensorMap &tm_b,
+                                     const CUtensorMap &tm_c, const TcArgs &p, const Geo &geo, const Plan &plan,
+                                     unsigned int *err) {
     using SM = TcSmem<MODE>;
     using TM = TcTmem<MODE>;
     extern __shared__ __align__(1024) uint8_t sm[];
@@ -334,7 +332,7 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     float *tabs = reinterpret_cast<float *>(sm + SM::TAB);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    const int ng = blockIdx.x % p.ng, sh = blockIdx.x / p.ng;
+    const int ng = bid % p.ng, sh = bid / p.ng;
     const int slot = sh / geo.H, h = sh - slot * geo.H;
     const int4 sl = slot_of(geo, plan, slot);
     const int t0 = sl.x, len = sl.y, c0 = ng * kN;
@@ -922,27 +920,29 @@ chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
 struct PairArgs {
     const float *g;
     float *rsum, *csum;  // [2, rows, H]
-    int H_k, dk, dv;
+    int dk, dv, split;
 };
 struct PairSmem {
     static constexpr uint32_t QK = 0, VO = 4 * kAtom, TAB = 8 * kAtom;
     static constexpr uint32_t BARS = TAB + 2 * kTab * 4, TOTAL = BARS + 8 * 8 + 16;
 };
 
-__global__ void __launch_bounds__(kPairThreads, 1)
-pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
-            PairArgs p, Geo geo, Plan plan, unsigned int *err) {
+__device__ __forceinline__ void pairs(unsigned int bid, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
+                                      const CUtensorMap &tm_v, const CUtensorMap &tm_o, const PairArgs &p,
+                                      const Geo &geo, const Plan &plan, unsigned int *err) {
+    // chunks first, first + split, ... of a (slot, head)
+    const int first = bid % p.split;
+    bid /= p.split;
     extern __shared__ __align__(1024) uint8_t sm[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + PairSmem::BARS);
     uint64_t *fullQ = bars, *fullV = bars + 1, *mdone = bars + 2, *tfull = bars + 3, *tfree = bars + 4;
     uint64_t *efree = bars + 5, *qdone = bars + 6;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + 8);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int slot = blockIdx.x / geo.H, h = blockIdx.x - slot * geo.H;
+    const int slot = bid / geo.H, h = bid - slot * geo.H;
     const int4 sl = slot_of(geo, plan, slot);
     const int t0 = sl.x, len = sl.y, nch = (len + kQ - 1) / kQ, hk = h / (geo.H / geo.Hk);
-    if (len <= 0 || (int)blockIdx.y >= nch) return;
+    if (len <= 0 || first >= nch) return;
     if (kChecked && !(chk_span(t0, len, geo.rows, err) && chk_span(slot, 1, geo.n_slots, err) &&
                       chk_true((smem_u32(sm) & 1023u) == 0, err)))
         return;
@@ -969,7 +969,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     if (warp == 0) {
         if (lane == 0) {
             int it = 0;
-            for (int cc = blockIdx.y; cc < nch; cc += gridDim.y, ++it) {
+            for (int cc = first; cc < nch; cc += p.split, ++it) {
                 const int y = t0 + cc * kQ;
                 if (it) ok = wait(qdone, (it - 1) & 1, err);
                 if (!ok) break;
@@ -997,7 +997,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         const uint64_t dv = sdesc_sw128(smem_u32(sm + PairSmem::VO), 16, 1024);
         int it = 0;
         // columns: Q K^T 0, K Q^T 128, dO V^T 256, V dO^T 384
-        for (int cc = blockIdx.y; cc < nch && ok; cc += gridDim.y, ++it) {
+        for (int cc = first; cc < nch && ok; cc += p.split, ++it) {
             if (it) ok = wait(efree, (it - 1) & 1, err);
 #pragma unroll 1
             for (int m = 0; m < 2 && ok; ++m) {
@@ -1025,8 +1025,8 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             for (int u = 0; u < 4; ++u)
                 gv[u] = 4 * lane + u < n ? load_g(geo, p.g, (long)t0 + cc * kQ + 4 * lane + u, h) : 0.f;
         };
-        load(blockIdx.y);
-        for (int cc = blockIdx.y; cc < nch; cc += gridDim.y, ++it) {
+        load(first);
+        for (int cc = first; cc < nch; cc += p.split, ++it) {
             if (it) ok = wait(tfree, (it - 1) & 1, err);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
@@ -1037,7 +1037,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 decay_tables<true>(tab, gv, lane);
             __syncwarp();
             if (lane == 0) mbar_arrive(tfull);
-            if (cc + (int)gridDim.y < nch) load(cc + gridDim.y);
+            if (cc + p.split < nch) load(cc + p.split);
         }
     } else {
         // rows (warps 4-11) or columns (12-19); two warps share a row's columns, 16 of each block each
@@ -1046,7 +1046,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         const uint32_t lb = (uint32_t)(rb * 32) << 16, col = rev ? 128 : 0;
         const float *tab = reinterpret_cast<const float *>(sm + PairSmem::TAB) + (rev ? kTab : 0);
         int it = 0;
-        for (int cc = blockIdx.y; cc < nch; cc += gridDim.y, ++it) {
+        for (int cc = first; cc < nch; cc += p.split, ++it) {
             const int n = min(kQ, len - cc * kQ);
             ok = ok && wait(tfull, it & 1, err);
             ok = ok && wait(qdone, it & 1, err);
@@ -1106,6 +1106,46 @@ pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     tc_fence_before();
     __syncthreads();
     if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------ launches
+// Walks of one kind.
+template <bool REV, int MODE>
+__global__ void __launch_bounds__(kTcThreads, 1)
+chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+             const __grid_constant__ CUtensorMap tm_c, TcArgs p, Geo geo, Plan plan, unsigned int *err) {
+    walk<REV, MODE>(blockIdx.x, tm_a, tm_b, tm_c, p, geo, plan, err);
+}
+struct Maps {
+    CUtensorMap q, k, v, o;
+};
+// Two kinds of work in one grid, so that the second's CTAs run on the SMs that the
+// first leaves: the blocks' states of both directions; dq and the pairs; dk and dv.
+// (Gradients of T 128, H 16, d 64: 37 us in a launch each, 24 us so; B 4, T 4096, d 128:
+// 413 us for the walks and pairs apart, 409 us together.)
+__global__ void __launch_bounds__(kTcThreads, 1)
+states_kernel(const __grid_constant__ Maps m, TcArgs p, TcArgs r, unsigned int n, Geo geo, Plan plan,
+              unsigned int *err) {
+    if (blockIdx.x < n)
+        walk<false, kStateOnly>(blockIdx.x, m.k, m.k, m.v, p, geo, plan, err);
+    else
+        walk<true, kStateOnly>(blockIdx.x - n, m.q, m.q, m.o, r, geo, plan, err);
+}
+__global__ void __launch_bounds__(kTcThreads, 1)
+dq_pairs_kernel(const __grid_constant__ Maps m, TcArgs p, PairArgs r, unsigned int n, Geo geo, Plan plan,
+                unsigned int *err) {
+    if (blockIdx.x < n)
+        walk<false, kOutDots>(blockIdx.x, m.o, m.v, m.k, p, geo, plan, err);
+    else
+        pairs(blockIdx.x - n, m.q, m.k, m.v, m.o, r, geo, plan, err);
+}
+__global__ void __launch_bounds__(kTcThreads, 1)
+dk_dv_kernel(const __grid_constant__ Maps m, TcArgs p, TcArgs r, unsigned int n, Geo geo, Plan plan,
+             unsigned int *err) {
+    if (blockIdx.x < n)
+        walk<true, kOutDots>(blockIdx.x, m.v, m.o, m.q, p, geo, plan, err);
+    else
+        walk<true, kOut>(blockIdx.x - n, m.k, m.q, m.o, r, geo, plan, err);
 }
 
 // ------------------------------------------------------------ gradient of the decays
@@ -1249,7 +1289,7 @@ int block_len(int n_seq, bool varlen, bool bwd, int T, int H, int ng, size_t nel
 }
 
 struct TcWs {
-    size_t slot, blk_start, gtot, X, Y, fin, ri, ci, rp, cp, bnd, ydot, dq32, dk32, part, total;
+    size_t slot, blk_start, gtot, gtot_rev, X, Y, fin, ri, ci, rp, cp, bnd, ydot, dq32, dk32, part, total;
     int L, nb, n_slots, multi, nbnd;
 };
 TcWs tc_ws(const LinCall &c, bool bwd) {
@@ -1274,6 +1314,7 @@ TcWs tc_ws(const LinCall &c, bool bwd) {
     w.slot = take(varlen ? sizeof(int4) * w.n_slots : 0);
     w.blk_start = take(varlen ? sizeof(int) * ((size_t)3 * n_seq + 1) : 0);
     w.gtot = take(w.multi ? sh * 4 : 0);
+    w.gtot_rev = take(bwd && w.multi ? sh * 4 : 0);
     w.X = take(w.multi ? sh * nel * 4 : 0);
     if (bwd) {
         w.Y = take(w.multi ? sh * nel * 4 : 0);
@@ -1314,28 +1355,35 @@ bool tile_map(CUtensorMap *m, const void *base, int d, int heads, size_t rows) {
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-struct Maps {
-    CUtensorMap q, k, v, o;
-};
 bool make_maps(Maps *m, const LinCall &c) {
     const size_t rows = (size_t)c.B * c.T;
     return tile_map(&m->q, c.q, c.dk_, c.Hk, rows) && tile_map(&m->k, c.k, c.dk_, c.Hk, rows) &&
            tile_map(&m->v, c.v, c.dv_, c.H, rows) && (!c.dout || tile_map(&m->o, c.dout, c.dv_, c.H, rows));
 }
 
+// the parts of a walk's arguments that follow from the others; its CTAs
+unsigned int prepare(const LinCall &c, const Geo &geo, TcArgs *p) {
+    p->g = c.g;
+    p->ng = groups(p->dc);
+    p->wide = ((uintptr_t)p->out & 31u) == 0;
+    return (unsigned)(geo.n_slots * geo.H * p->ng);
+}
+template <typename K>
+cudaError_t allow(gdr_host::SmemLimit *limit, K kernel) {
+    constexpr int most = TcSmem<kOut>::TOTAL > TcSmem<kOutDots>::TOTAL ? TcSmem<kOut>::TOTAL : TcSmem<kOutDots>::TOTAL;
+    static_assert(PairSmem::TOTAL <= most && TcSmem<kStateOnly>::TOTAL <= most, "shared memory");
+    return limit->set((const void *)kernel, most);
+}
+
 template <bool REV, int MODE>
 cudaError_t launch_chain(const LinCall &c, const Geo &geo, const Plan &plan, const CUtensorMap &a,
                          const CUtensorMap &b, const CUtensorMap &cc, TcArgs p, int id) {
-    const size_t smem = TcSmem<MODE>::TOTAL;
     static gdr_host::SmemLimit limit;
-    const cudaError_t e = limit.set((const void *)chain_kernel<REV, MODE>, (int)smem);
+    const cudaError_t e = allow(&limit, chain_kernel<REV, MODE>);
     if (e != cudaSuccess) return e;
-    p.g = c.g;
-    p.ng = groups(p.dc);
-    p.wide = ((uintptr_t)p.out & 31u) == 0;
+    const unsigned int n = prepare(c, geo, &p);
     gdr_host::ProfToken tk = gdr_host::prof_begin(id, c.st);
-    chain_kernel<REV, MODE><<<(unsigned)(geo.n_slots * geo.H * p.ng), kTcThreads, smem, c.st>>>(
-        a, b, cc, p, geo, plan, c.err);
+    chain_kernel<REV, MODE><<<n, kTcThreads, TcSmem<MODE>::TOTAL, c.st>>>(a, b, cc, p, geo, plan, c.err);
     gdr_host::prof_end(tk, c.st);
     return cudaGetLastError();
 }
@@ -1391,21 +1439,30 @@ cudaError_t lin_bwd_tc(const LinCall &c) {
     float *ri = (float *)(c.ws + w.ri), *ci = (float *)(c.ws + w.ci);
     float *rp = (float *)(c.ws + w.rp), *cp = (float *)(c.ws + w.cp);
     float *part = c.gate == GDR_GATE_HEAD ? (float *)(c.ws + w.part) : nullptr;
+    static SmemLimit lim_s, lim_q, lim_k;
+    ProfToken tk;
     if (w.multi) {
         TcArgs s{};
         s.ha = s.hb = c.Hk; s.hc = c.H; s.he = c.H;
         s.db = c.dk_; s.dc = c.dv_;
-        s.gtot = (float *)(c.ws + w.gtot);
+        TcArgs t = s;
         s.xout = X;
-        if ((e = launch_chain<false, kStateOnly>(c, geo, plan, m.k, m.k, m.v, s, GDR_K_LIN_STATE)) != cudaSuccess)
-            return e;
+        t.xout = Y;
+        s.gtot = (float *)(c.ws + w.gtot);
+        t.gtot = (float *)(c.ws + w.gtot_rev);
+        if ((e = allow(&lim_s, states_kernel)) != cudaSuccess) return e;
+        const unsigned int n = prepare(c, geo, &s);
+        prepare(c, geo, &t);
+        tk = prof_begin(GDR_K_LIN_STATE, c.st);
+        states_kernel<<<2 * n, kTcThreads, TcSmem<kStateOnly>::TOTAL, c.st>>>(m, s, t, n, geo, plan, c.err);
+        prof_end(tk, c.st);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
         if ((e = lin_scan(c, geo, l, X, c.S0, nullptr, false)) != cudaSuccess) return e;
-        s.xout = Y;
-        if ((e = launch_chain<true, kStateOnly>(c, geo, plan, m.q, m.q, m.o, s, GDR_K_LIN_STATE)) != cudaSuccess)
-            return e;
-        if ((e = lin_scan(c, geo, l, Y, c.dS_final, nullptr, true)) != cudaSuccess) return e;
+        LinWs back = l;
+        back.gtot = w.gtot_rev;
+        if ((e = lin_scan(c, geo, back, Y, c.dS_final, nullptr, true)) != cudaSuccess) return e;
     }
-    // dq: (a, b, c) = (dout, v, k), the state transposed
+    // dq: (a, b, c) = (dout, v, k), the state transposed; beside it the pairs inside chunks
     TcArgs p{};
     p.ha = p.hb = c.H; p.hc = p.he = c.Hk;
     p.db = c.dv_; p.dc = c.dk_; p.tr = 1;
@@ -1419,26 +1476,9 @@ cudaError_t lin_bwd_tc(const LinCall &c) {
     p.bnd = (float *)(c.ws + w.bnd);
     p.ydot = (float *)(c.ws + w.ydot);
     p.nbnd = w.nbnd;
-    if ((e = launch_chain<false, kOutDots>(c, geo, plan, m.o, m.v, m.k, p, GDR_K_LIN_GRAD)) != cudaSuccess)
-        return e;
-    // dk: (v, dout, q), backward in time
-    p.xin = c.dS_final;
-    p.xblk = Y;
-    p.xout = nullptr;
-    p.out = shared ? (void *)(c.ws + w.dk32) : c.dk;
-    p.e = k;
-    p.dots = ci;
-    if ((e = launch_chain<true, kOutDots>(c, geo, plan, m.v, m.o, m.q, p, GDR_K_LIN_GRAD)) != cudaSuccess)
-        return e;
-    if (shared) {
-        if ((e = lin_group_sum(c, geo, l, (const float *)(c.ws + w.dq32), c.dq, c.dk_)) != cudaSuccess) return e;
-        if ((e = lin_group_sum(c, geo, l, (const float *)(c.ws + w.dk32), c.dk, c.dk_)) != cudaSuccess) return e;
-    }
-    static SmemLimit limit;
-    if ((e = limit.set((const void *)pair_kernel, (int)PairSmem::TOTAL)) != cudaSuccess) return e;
+    // pairs: CTAs for a (slot, head), as many as end soonest on 148 SMs, a start costing about as
+    // much as one and a half chunks (B4 T4096 H16 d128: two, 191 us with dq's walks; four 200)
     const long units = (long)geo.n_slots * geo.H, most = w.L / kQ;
-    // chunks of a (slot, head) per CTA: the number of CTAs that ends soonest on 148 SMs, a start
-    // costing about as much as one and a half chunks
     long split = 1;
     double least = 1e30;
     for (long n = 1; n <= most && n <= 64; ++n) {
@@ -1448,12 +1488,42 @@ cudaError_t lin_bwd_tc(const LinCall &c) {
             split = n;
         }
     }
-    PairArgs pa{c.g, rp, cp, c.Hk, c.dk_, c.dv_};
-    ProfToken tk = prof_begin(GDR_K_LIN_GRAD, c.st);
-    pair_kernel<<<dim3((unsigned)units, (unsigned)split), kPairThreads, PairSmem::TOTAL, c.st>>>(
-        m.q, m.k, m.v, m.o, pa, geo, plan, c.err);
+    const PairArgs pa{c.g, rp, cp, c.dk_, c.dv_, (int)split};
+    if ((e = allow(&lim_q, dq_pairs_kernel)) != cudaSuccess) return e;
+    unsigned int n = prepare(c, geo, &p);
+    tk = prof_begin(GDR_K_LIN_GRAD, c.st);
+    dq_pairs_kernel<<<n + (unsigned)(units * split), kTcThreads, TcSmem<kOutDots>::TOTAL, c.st>>>(m, p, pa, n, geo,
+                                                                                               plan, c.err);
     prof_end(tk, c.st);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    // dk: (v, dout, q), backward in time
+    p.xin = c.dS_final;
+    p.xblk = Y;
+    p.xout = nullptr;
+    p.out = shared ? (void *)(c.ws + w.dk32) : c.dk;
+    p.e = k;
+    p.dots = ci;
+    // dv: (k, q, dout), backward in time; beside dk, unless dS0 is to be written over dS_final
+    TcArgs r{};
+    r.ha = r.hb = c.Hk; r.hc = r.he = c.H;
+    r.db = c.dk_; r.dc = c.dv_;
+    r.xin = c.dS_final;
+    r.xblk = Y;
+    r.xout = c.dS0;
+    r.out = c.dv;
+    const bool over = c.dS0 && c.dS0 == c.dS_final;
+    if ((e = allow(&lim_k, dk_dv_kernel)) != cudaSuccess) return e;
+    n = prepare(c, geo, &p);
+    const unsigned int nv = prepare(c, geo, &r);
+    static_assert(TcSmem<kOutDots>::TOTAL >= TcSmem<kOut>::TOTAL, "shared memory");
+    tk = prof_begin(GDR_K_LIN_GRAD, c.st);
+    dk_dv_kernel<<<n + (over ? 0 : nv), kTcThreads, TcSmem<kOutDots>::TOTAL, c.st>>>(m, p, r, n, geo, plan, c.err);
+    prof_end(tk, c.st);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (shared) {
+        if ((e = lin_group_sum(c, geo, l, (const float *)(c.ws + w.dq32), c.dq, c.dk_)) != cudaSuccess) return e;
+        if ((e = lin_group_sum(c, geo, l, (const float *)(c.ws + w.dk32), c.dk, c.dk_)) != cudaSuccess) return e;
+    }
     DgArgs d{ri, ci, rp, cp, (const float *)(c.ws + w.ydot), 2 * groups(c.dk_), 2 * groups(c.dk_),
              8 * groups(c.dk_), fin, c.dS_final, c.dg, part, c.dk_ * c.dv_, w.nbnd};
     tk = prof_begin(GDR_K_LIN_GRAD, c.st);
@@ -1465,15 +1535,7 @@ cudaError_t lin_bwd_tc(const LinCall &c) {
         by_run.n_slots = geo.n_slots * w.nbnd;
         if ((e = lin_dg_heads(c, by_run, part)) != cudaSuccess) return e;
     }
-    // dv: (k, q, dout), backward in time; last, since dS0 may be written over dS_final
-    TcArgs r{};
-    r.ha = r.hb = c.Hk; r.hc = r.he = c.H;
-    r.db = c.dk_; r.dc = c.dv_;
-    r.xin = c.dS_final;
-    r.xblk = Y;
-    r.xout = c.dS0;
-    r.out = c.dv;
-    return launch_chain<true, kOut>(c, geo, plan, m.k, m.q, m.o, r, GDR_K_LIN_GRAD);
+    return over ? launch_chain<true, kOut>(c, geo, plan, m.k, m.q, m.o, r, GDR_K_LIN_GRAD) : cudaSuccess;
 }
 
 }  // namespace gdr_host
