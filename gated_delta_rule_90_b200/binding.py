@@ -407,34 +407,55 @@ def _linear_bad(dev, name, t, dtype, shape):
     raise ValueError("tensors must be contiguous")
 
 
-def _linear_args(q, k, v, g, tensors):
-    """Shapes and checks shared by the linear attention calls: q, k
-    [*lead, H_k, d_k], v [*lead, H, d_v], g [*lead, H] or [H]; ``tensors`` are
-    further ``(name, tensor, dtype, shape)``.  Every shape must match, every
-    tensor be contiguous and on q's device.  (A call for one token takes the
-    host about as long as the GPU: one expression per tensor, the message made
-    afterwards.)"""
+def _linear_refuse(q, k, v, g):
+    """The reason why _linear_args does not take q, k, v, g, if there is one."""
     if not (isinstance(q, torch.Tensor) and q.is_cuda):
         raise ValueError("tensors must be CUDA tensors")
     for name, t in (("v", v), ("g", g)):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
-    dev, at, qs, vs, tok = q.device, q.get_device(), q.shape, v.shape, q.dtype
-    *lead, H_k, d_k = qs
-    H, d_v = vs[-2:]
-    gate = GDR_GATE_HEAD if g.dim() == 1 else GDR_GATE_SCALAR
+    dev, lead, H, d_v = q.device, q.shape[:-2], v.shape[-2], v.shape[-1]
     if g.dim() == len(lead) + 2:
         raise ValueError("linear attention takes one decay per head ([..., H] or [H]), "
                          "not one per key channel")
-    if H_k < 1 or H % H_k:
-        raise ValueError(f"{H} value heads do not share {H_k} query/key heads evenly")
-    for spec in (("q", q, tok, qs), ("k", k, tok, qs), ("v", v, tok, (*lead, H, d_v)),
-                 ("g", g, torch.float32, (H,) if gate else (*lead, H)), *tensors):
+    for name, t, dtype, shape in (("q", q, q.dtype, q.shape), ("k", k, q.dtype, q.shape),
+                                  ("v", v, q.dtype, (*lead, H, d_v)),
+                                  ("g", g, torch.float32, (H,) if g.dim() == 1 else (*lead, H))):
+        if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype == dtype and
+                t.is_contiguous() and t.device == dev):
+            _linear_bad(dev, name, t, dtype, shape)
+
+
+def _linear_args(q, k, v, g, tensors):
+    """Shapes and checks shared by the linear attention calls: q, k
+    [*lead, H_k, d_k], v [*lead, H, d_v], g [*lead, H] or [H]; ``tensors`` are
+    further ``(name, tensor, dtype, shape)``.  Every shape must match, every
+    tensor be contiguous and on q's device.  (A call for one token takes the
+    host longer than the GPU, so everything is tested in one expression and the
+    message made afterwards.)"""
+    try:
+        at, qs, vs, gs, tok, f32 = q.get_device(), q.shape, v.shape, g.shape, q.dtype, torch.float32
+        good = (at >= 0 and k.shape == qs and len(vs) == len(qs) and vs[:-2] == qs[:-2] and
+                (gs == vs[:-1] or len(gs) == 1 and gs[0] == vs[-2]) and
+                k.dtype is tok and v.dtype is tok and g.dtype is f32 and
+                k.get_device() == at and v.get_device() == at and g.get_device() == at and
+                q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and g.is_contiguous())
+    except AttributeError:  # not tensors
+        good = False
+    if not good:
+        _linear_refuse(q, k, v, g)
+        raise ValueError("q, k, v and g do not match")
+    dev = q.device
+    for spec in tensors:
         t = spec[1]
         if t is not None and not (isinstance(t, torch.Tensor) and t.shape == spec[3] and
                                   t.dtype is spec[2] and t.is_contiguous() and t.get_device() == at):
             _linear_bad(dev, *spec)
-    return dev, _dtype_code(q), gate, H, H_k, d_k, d_v
+    H_k, d_k, H, d_v = qs[-2], qs[-1], vs[-2], vs[-1]
+    if H_k < 1 or H % H_k:
+        raise ValueError(f"{H} value heads do not share {H_k} query/key heads evenly")
+    code = GDR_BF16 if tok is torch.bfloat16 else _dtype_code(q)
+    return dev, code, GDR_GATE_HEAD if len(gs) == 1 else GDR_GATE_SCALAR, H, H_k, d_k, d_v
 
 
 def _addr(t):
@@ -456,16 +477,16 @@ def _linear_call(dev, stream, ws_bytes, workspace, call):
             ws, n = torch.empty(ws_bytes, dtype=torch.uint8, device=dev), ws_bytes
         return call(_addr(ws), n, handle)
 
-    if stream is not None:
-        handle = _stream(stream, dev).value or 0
-        s = stream if isinstance(stream, torch.cuda.Stream) else \
-            torch.cuda.ExternalStream(handle, device=dev)
-        with torch.cuda.device(dev), torch.cuda.stream(s):
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(dev.index)
+        if torch.cuda.current_device() == dev.index:
             return go(handle)
-    handle = torch._C._cuda_getCurrentRawStream(dev.index)
-    if torch.cuda.current_device() == dev.index:
-        return go(handle)
-    with torch.cuda.device(dev):
+        with torch.cuda.device(dev):
+            return go(handle)
+    handle = _stream(stream, dev).value or 0
+    s = stream if isinstance(stream, torch.cuda.Stream) else \
+        torch.cuda.ExternalStream(handle, device=dev)
+    with torch.cuda.device(dev), torch.cuda.stream(s):
         return go(handle)
 
 

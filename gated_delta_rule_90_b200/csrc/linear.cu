@@ -79,10 +79,17 @@ plan_kernel(const int32_t *__restrict__ cu, Geo geo, int4 *__restrict__ slot,
 // (sequence, head), leaving in X the state that enters each block.  HBM-bound:
 // X is read and written once.  A thread holds 4 elements; loads run 4 blocks
 // ahead of the carry.
+struct ScanArgs {
+    float *X;
+    const float *gtot, *init;
+    float *fin;
+};
 template <bool REV>
-__global__ void __launch_bounds__(256)
-scan_kernel(float *__restrict__ X, const float *__restrict__ gtot, const float *__restrict__ init,
-            float *__restrict__ fin, Geo geo, Plan plan, int nel, unsigned int *err) {
+__device__ __forceinline__ void scan(const ScanArgs &p, const Geo &geo, const Plan &plan, int nel,
+                                     unsigned int *err) {
+    float *__restrict__ X = p.X;
+    const float *__restrict__ gtot = p.gtot, *__restrict__ init = p.init;
+    float *__restrict__ fin = p.fin;
     const int s = blockIdx.x / geo.H, h = blockIdx.x - s * geo.H;
     const int el = (blockIdx.y * 256 + threadIdx.x) * 4;
     const int first = geo.varlen ? plan.blk_start[s] : s * geo.nb;
@@ -115,6 +122,14 @@ scan_kernel(float *__restrict__ X, const float *__restrict__ gtot, const float *
             }
     }
     if (fin) *reinterpret_cast<float4 *>(fin + so) = S;
+}
+// forward in time (blockIdx.z below nf), then backward
+__global__ void __launch_bounds__(256)
+scan_kernel(ScanArgs f, ScanArgs r, int nf, Geo geo, Plan plan, int nel, unsigned int *err) {
+    if ((int)blockIdx.z < nf)
+        scan<false>(f, geo, plan, nel, err);
+    else
+        scan<true>(r, geo, plan, nel, err);
 }
 
 // ------------------------------------------------------------ sums
@@ -353,19 +368,16 @@ cudaError_t lin_plan(const LinCall &c, const Geo &geo, const LinWs &w) {
     return cudaGetLastError();
 }
 
-cudaError_t lin_scan(const LinCall &c, const Geo &geo, const LinWs &w, float *X, const float *init,
-                     float *fin, bool rev) {
-    if (!geo.n_slots && !fin) return cudaSuccess;
+cudaError_t lin_scan(const LinCall &c, const Geo &geo, const LinWs &w, const LinScan *f, const LinScan *r) {
+    if (!geo.n_slots && !(f && f->fin) && !(r && r->fin)) return cudaSuccess;
     const int nel = c.dk_ * c.dv_;
     const Plan plan = {(const int4 *)(c.ws + w.slot), (const int *)(c.ws + w.blk_start)};
-    const dim3 grid((unsigned)(geo.n_seq * geo.H), (unsigned)((nel / 4 + 255) / 256));
+    const dim3 grid((unsigned)(geo.n_seq * geo.H), (unsigned)((nel / 4 + 255) / 256), f && r ? 2 : 1);
+    ScanArgs a{}, b{};
+    if (f) a = {f->X, f->gtot, f->init, f->fin};
+    if (r) b = {r->X, r->gtot, r->init, r->fin};
     ProfToken tk = prof_begin(GDR_K_LIN_SCAN, c.st);
-    if (rev)
-        scan_kernel<true><<<grid, 256, 0, c.st>>>(X, (const float *)(c.ws + w.gtot), init, fin, geo,
-                                                  plan, nel, c.err);
-    else
-        scan_kernel<false><<<grid, 256, 0, c.st>>>(X, (const float *)(c.ws + w.gtot), init, fin, geo,
-                                                   plan, nel, c.err);
+    scan_kernel<<<grid, 256, 0, c.st>>>(a, b, f ? 1 : 0, geo, plan, nel, c.err);
     prof_end(tk, c.st);
     return cudaGetLastError();
 }

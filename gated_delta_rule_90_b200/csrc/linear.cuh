@@ -88,10 +88,16 @@ LinWs lin_ws(int B, int T, int H, int Hk, int dk, int dv, int n_seq, bool varlen
 gdr::lin::Geo lin_geo(const LinCall &c, const LinWs &w);
 cudaError_t lin_plan(const LinCall &c, const gdr::lin::Geo &geo, const LinWs &w);
 // States of the blocks carried over each sequence: X[slot] (the block's own
-// contribution) becomes the state that enters the block; forward in time from
-// `init`, or backward (rev).  `fin` (may be NULL) receives the last state.
-cudaError_t lin_scan(const LinCall &c, const gdr::lin::Geo &geo, const LinWs &w, float *X,
-                     const float *init, float *fin, bool rev);
+// contribution) becomes the state that enters the block, from `init` on; `fin` (may
+// be NULL) receives the last state.  Forward in time (f), backward (r), or both in
+// one launch.
+struct LinScan {
+    float *X;
+    const float *gtot, *init;
+    float *fin;
+};
+cudaError_t lin_scan(const LinCall &c, const gdr::lin::Geo &geo, const LinWs &w, const LinScan *f,
+                     const LinScan *r);
 cudaError_t lin_group_sum(const LinCall &c, const gdr::lin::Geo &geo, const LinWs &w,
                           const float *x, void *out, int d);
 cudaError_t lin_dg_heads(const LinCall &c, const gdr::lin::Geo &geo, const float *part);

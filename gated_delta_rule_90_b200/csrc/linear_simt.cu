@@ -17,9 +17,9 @@
 // sum again in each block of 256 keeps its rounding from growing with the
 // sequence.
 //
-// Blocks of 256 tokens run in parallel: their own contribution to the state
-// (state_kernel), the carry over the blocks (lin_scan), the outputs
-// (out_kernel, 32-token chunks in order).
+// Blocks of up to 256 tokens run in parallel: their own contribution to the state
+// (state_kernel), the carry over the blocks (lin_scan), the outputs (out_kernel,
+// grad_kernel, 32-token chunks in order).
 #include "linear.cuh"
 
 namespace gdr {
@@ -66,15 +66,21 @@ __device__ __forceinline__ void block_decays(const Geo &geo, const float *g, lon
 // (forward: b, c = k, v) or e^{G_j} (REV: b, c = q, dout); rows are value
 // channels, columns key channels.  A thread holds a 4 x 4 tile; per token two
 // 16-byte shared reads feed 16 FMAs.
+template <typename T>
+struct StateArgs {
+    const T *b, *c;
+    float *X;
+};
 template <typename T, bool REV>
-__global__ void __launch_bounds__(kThreads)
-state_kernel(const T *__restrict__ b, const T *__restrict__ c, const float *__restrict__ g,
-             float *__restrict__ X, float *__restrict__ gtot, Geo geo, Plan plan, int db, int dc,
-             unsigned int *err) {
+__device__ __forceinline__ void block_state(const StateArgs<T> &p, int z, const float *__restrict__ g,
+                                            float *__restrict__ gtot, const Geo &geo, const Plan &plan, int db,
+                                            int dc, unsigned int *err) {
+    const T *__restrict__ b = p.b, *__restrict__ c = p.c;
+    float *__restrict__ X = p.X;
     __shared__ double sG[kBlk + 1];
     __shared__ __align__(16) float sb[kC * 128];
     __shared__ __align__(16) float sc[kC * kNb];
-    const int slot = blockIdx.x, h = blockIdx.y, c0 = blockIdx.z * kNb, tid = threadIdx.x;
+    const int slot = blockIdx.x, h = blockIdx.y, c0 = z * kNb, tid = threadIdx.x;
     const int4 sl = slot_of(geo, plan, slot);
     const long t0 = sl.x;
     const int len = sl.y;
@@ -130,6 +136,18 @@ state_kernel(const T *__restrict__ b, const T *__restrict__ c, const float *__re
     if (c0 == 0 && tid == 0 && gtot) gtot[(size_t)slot * geo.H + h] = (float)sG[len];
 }
 
+// forward (blockIdx.z below nz), then reverse
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+state_kernel(StateArgs<T> f, StateArgs<T> r, int nz, const float *__restrict__ g, float *__restrict__ gtot,
+             Geo geo, Plan plan, int db, int dc, unsigned int *err) {
+    const int z = blockIdx.z;
+    if (z < nz)
+        block_state<T, false>(f, z, g, gtot, geo, plan, db, dc, err);
+    else
+        block_state<T, true>(r, z - nz, g, nullptr, geo, plan, db, dc, err);
+}
+
 // ------------------------------------------------------------ outputs
 template <typename T>
 struct Roles {
@@ -137,12 +155,17 @@ struct Roles {
     int ha, hb, hc, he;      // their heads
     int db, dc;
     bool tr;                 // X is the transpose of the stored [d_v, d_k] state
+    const float *X;
+    void *out;
+    float *dots;
 };
 
 template <typename T, typename To, bool REV>
-__global__ void __launch_bounds__(kThreads)
-out_kernel(Roles<T> ro, const float *__restrict__ g, const float *__restrict__ X,
-           To *__restrict__ out, float *__restrict__ dots, Geo geo, Plan plan, unsigned int *err) {
+__device__ __forceinline__ void outputs(const Roles<T> &ro, int z, const float *__restrict__ g, const Geo &geo,
+                                        const Plan &plan, unsigned int *err) {
+    const float *__restrict__ X = ro.X;
+    To *__restrict__ out = (To *)ro.out;
+    float *__restrict__ dots = ro.dots;
     extern __shared__ __align__(16) float sm[];
     __shared__ double sG[kBlk + 1];
     __shared__ float sInter[kC], sW[kC];
@@ -150,7 +173,7 @@ out_kernel(Roles<T> ro, const float *__restrict__ g, const float *__restrict__ X
     constexpr int ldc = kC + 4;
     float *sa = sm, *sb = sa + kC * lda, *sX = sb + kC * lda;
     float *sP = sX + kNb * lda, *sc = sP + kC * ldc, *sct = sc + kC * ldc;
-    const int slot = blockIdx.x, h = blockIdx.y, c0 = blockIdx.z * kNb, tid = threadIdx.x;
+    const int slot = blockIdx.x, h = blockIdx.y, c0 = z * kNb, tid = threadIdx.x;
     const int4 sl = slot_of(geo, plan, slot);
     const long t0 = sl.x;
     const int len = sl.y;
@@ -270,7 +293,7 @@ out_kernel(Roles<T> ro, const float *__restrict__ g, const float *__restrict__ X
 #pragma unroll
                 for (int k = 8; k; k >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, k);
                 if (tj == 0 && i < n)
-                    dots[((size_t)blockIdx.z * geo.rows + row) * geo.H + h] = dot;
+                    dots[((size_t)z * geo.rows + row) * geo.H + h] = dot;
             }
         }
         if (cc == nch - 1) break;
@@ -303,6 +326,26 @@ out_kernel(Roles<T> ro, const float *__restrict__ g, const float *__restrict__ X
             }
         }
     }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+out_kernel(Roles<T> ro, const float *__restrict__ g, Geo geo, Plan plan, unsigned int *err) {
+    outputs<T, T, false>(ro, blockIdx.z, g, geo, plan, err);
+}
+// dq (blockIdx.z below nq), dk (below 2 nq), dv in one launch: a short step waited for each
+// (T 100, H 4, d 64: 55 us with a launch each, 38 us so and with states and carries in pairs)
+template <typename T, typename To>
+__global__ void __launch_bounds__(kThreads)
+grad_kernel(Roles<T> rq, Roles<T> rk, Roles<T> rv, int nq, const float *__restrict__ g, Geo geo, Plan plan,
+            unsigned int *err) {
+    const int z = blockIdx.z;
+    if (z < nq)
+        outputs<T, To, false>(rq, z, g, geo, plan, err);
+    else if (z < 2 * nq)
+        outputs<T, To, true>(rk, z - nq, g, geo, plan, err);
+    else
+        outputs<T, T, true>(rv, z - 2 * nq, g, geo, plan, err);
 }
 
 // ------------------------------------------------------------ gradient of the decays
@@ -385,7 +428,7 @@ Plan plan_of(const gdr_host::LinCall &c, const gdr_host::LinWs &w) {
 
 gdr_host::LinWs simt_ws(const gdr_host::LinCall &c, bool bwd) {
     // Blocks of up to 256 tokens; of fewer, down to one chunk, while the grid would leave SMs idle:
-    // a block's chunks run one after another (gradients of T 100, H 4, d 64: 107 us in blocks of 256, 55 us of 32)
+    // a block's chunks run one after another (gradients of T 100, H 4, d 64: 107 us in blocks of 256, 57 us of 32)
     int L = kBlk;
     while (L > kC) {
         const double slots = c.cu ? (double)c.T / L + c.n_seq : (double)c.B * ((c.T + L - 1) / L);
@@ -396,28 +439,14 @@ gdr_host::LinWs simt_ws(const gdr_host::LinCall &c, bool bwd) {
                             blocks_of(c.dk_) > blocks_of(c.dv_) ? blocks_of(c.dk_) : blocks_of(c.dv_));
 }
 
-template <typename T, bool REV>
-cudaError_t launch_state(const gdr_host::LinCall &c, const Geo &geo, const Plan &plan, const void *b,
-                         const void *v, float *X, float *gtot) {
+template <typename T>
+cudaError_t launch_states(const gdr_host::LinCall &c, const Geo &geo, const Plan &plan, const StateArgs<T> &f,
+                          const StateArgs<T> *r, float *gtot) {
     if (!geo.n_slots) return cudaSuccess;
+    const int nz = blocks_of(c.dv_);
     gdr_host::ProfToken tk = gdr_host::prof_begin(GDR_K_LIN_STATE, c.st);
-    state_kernel<T, REV><<<dim3(geo.n_slots, c.H, blocks_of(c.dv_)), kThreads, 0, c.st>>>(
-        (const T *)b, (const T *)v, c.g, X, gtot, geo, plan, c.dk_, c.dv_, c.err);
-    gdr_host::prof_end(tk, c.st);
-    return cudaGetLastError();
-}
-
-template <typename T, typename To, bool REV>
-cudaError_t launch_out(const gdr_host::LinCall &c, const Geo &geo, const Plan &plan,
-                       const Roles<T> &ro, const float *X, void *out, float *dots, int id) {
-    if (!geo.n_slots) return cudaSuccess;
-    const size_t smem = out_smem(ro.db);
-    static gdr_host::SmemLimit limit;
-    const cudaError_t e = limit.set((const void *)out_kernel<T, To, REV>, (int)out_smem(128));
-    if (e != cudaSuccess) return e;
-    gdr_host::ProfToken tk = gdr_host::prof_begin(id, c.st);
-    out_kernel<T, To, REV><<<dim3(geo.n_slots, c.H, blocks_of(ro.dc)), kThreads, smem, c.st>>>(
-        ro, c.g, X, (To *)out, dots, geo, plan, c.err);
+    state_kernel<T><<<dim3(geo.n_slots, c.H, r ? 2 * nz : nz), kThreads, 0, c.st>>>(
+        f, r ? *r : f, nz, c.g, gtot, geo, plan, c.dk_, c.dv_, c.err);
     gdr_host::prof_end(tk, c.st);
     return cudaGetLastError();
 }
@@ -430,11 +459,34 @@ cudaError_t fwd_t(const gdr_host::LinCall &c) {
     float *X = (float *)(c.ws + w.X), *gtot = (float *)(c.ws + w.gtot);
     cudaError_t e;
     if ((e = gdr_host::lin_plan(c, geo, w)) != cudaSuccess) return e;
-    if ((e = launch_state<T, false>(c, geo, plan, c.k, c.v, X, gtot)) != cudaSuccess) return e;
-    if ((e = gdr_host::lin_scan(c, geo, w, X, c.S0, c.S_final, false)) != cudaSuccess) return e;
-    const Roles<T> ro = {(const T *)c.q, (const T *)c.k, (const T *)c.v, nullptr,
-                         c.Hk, c.Hk, c.H, c.H, c.dk_, c.dv_, false};
-    return launch_out<T, T, false>(c, geo, plan, ro, X, c.out, nullptr, GDR_K_LIN_OUT);
+    if ((e = launch_states<T>(c, geo, plan, {(const T *)c.k, (const T *)c.v, X}, nullptr, gtot)) != cudaSuccess)
+        return e;
+    const gdr_host::LinScan f{X, gtot, c.S0, c.S_final};
+    if ((e = gdr_host::lin_scan(c, geo, w, &f, nullptr)) != cudaSuccess) return e;
+    if (!geo.n_slots) return cudaSuccess;
+    const Roles<T> ro = {(const T *)c.q, (const T *)c.k, (const T *)c.v, nullptr, c.Hk, c.Hk, c.H, c.H,
+                         c.dk_, c.dv_, false, X, c.out, nullptr};
+    static gdr_host::SmemLimit limit;
+    if ((e = limit.set((const void *)out_kernel<T>, (int)out_smem(128))) != cudaSuccess) return e;
+    gdr_host::ProfToken tk = gdr_host::prof_begin(GDR_K_LIN_OUT, c.st);
+    out_kernel<T><<<dim3(geo.n_slots, c.H, blocks_of(c.dv_)), kThreads, out_smem(c.dk_), c.st>>>(ro, c.g, geo, plan,
+                                                                                              c.err);
+    gdr_host::prof_end(tk, c.st);
+    return cudaGetLastError();
+}
+
+template <typename T, typename To>
+cudaError_t launch_grads(const gdr_host::LinCall &c, const Geo &geo, const Plan &plan, const Roles<T> &rq,
+                         const Roles<T> &rk, const Roles<T> &rv) {
+    static gdr_host::SmemLimit limit;
+    const cudaError_t e = limit.set((const void *)grad_kernel<T, To>, (int)out_smem(128));
+    if (e != cudaSuccess) return e;
+    const int nq = blocks_of(c.dk_);
+    gdr_host::ProfToken tk = gdr_host::prof_begin(GDR_K_LIN_GRAD, c.st);
+    grad_kernel<T, To><<<dim3(geo.n_slots, c.H, 2 * nq + blocks_of(c.dv_)), kThreads,
+                         out_smem(c.dk_ > c.dv_ ? c.dk_ : c.dv_), c.st>>>(rq, rk, rv, nq, c.g, geo, plan, c.err);
+    gdr_host::prof_end(tk, c.st);
+    return cudaGetLastError();
 }
 
 template <typename T>
@@ -450,30 +502,23 @@ cudaError_t bwd_t(const gdr_host::LinCall &c) {
     const T *q = (const T *)c.q, *k = (const T *)c.k, *v = (const T *)c.v, *dy = (const T *)c.dout;
     cudaError_t e;
     if ((e = gdr_host::lin_plan(c, geo, w)) != cudaSuccess) return e;
-    if ((e = launch_state<T, false>(c, geo, plan, k, v, X, gtot)) != cudaSuccess) return e;
-    if ((e = launch_state<T, true>(c, geo, plan, q, dy, Y, nullptr)) != cudaSuccess) return e;
-    if ((e = gdr_host::lin_scan(c, geo, w, X, c.S0, fin, false)) != cudaSuccess) return e;
-    if ((e = gdr_host::lin_scan(c, geo, w, Y, c.dS_final, c.dS0, true)) != cudaSuccess) return e;
-    const Roles<T> rq = {dy, v, k, q, c.H, c.H, c.Hk, c.Hk, c.dv_, c.dk_, true};
-    const Roles<T> rk = {v, dy, q, nullptr, c.H, c.H, c.Hk, c.Hk, c.dv_, c.dk_, true};
-    const Roles<T> rv = {k, q, dy, v, c.Hk, c.Hk, c.H, c.H, c.dk_, c.dv_, false};
-    if (shared) {  // per value head in fp32, then summed
-        e = launch_out<T, float, false>(c, geo, plan, rq, X, c.ws + w.dq32, rdot, GDR_K_LIN_GRAD);
-        if (e == cudaSuccess)
-            e = launch_out<T, float, true>(c, geo, plan, rk, Y, c.ws + w.dk32, nullptr, GDR_K_LIN_GRAD);
-        if (e == cudaSuccess)
-            e = gdr_host::lin_group_sum(c, geo, w, (const float *)(c.ws + w.dq32), c.dq, c.dk_);
-        if (e == cudaSuccess)
-            e = gdr_host::lin_group_sum(c, geo, w, (const float *)(c.ws + w.dk32), c.dk, c.dk_);
-    } else {
-        e = launch_out<T, T, false>(c, geo, plan, rq, X, c.dq, rdot, GDR_K_LIN_GRAD);
-        if (e == cudaSuccess)
-            e = launch_out<T, T, true>(c, geo, plan, rk, Y, c.dk, nullptr, GDR_K_LIN_GRAD);
-    }
-    if (e == cudaSuccess)
-        e = launch_out<T, T, true>(c, geo, plan, rv, Y, c.dv, cdot, GDR_K_LIN_GRAD);
-    if (e != cudaSuccess) return e;
+    const StateArgs<T> back{q, dy, Y};
+    if ((e = launch_states<T>(c, geo, plan, {k, v, X}, &back, gtot)) != cudaSuccess) return e;
+    const gdr_host::LinScan f{X, gtot, c.S0, fin}, b{Y, gtot, c.dS_final, c.dS0};
+    if ((e = gdr_host::lin_scan(c, geo, w, &f, &b)) != cudaSuccess) return e;
     if (geo.n_slots) {
+        // of shared query/key heads per value head in fp32, then summed
+        const Roles<T> rq = {dy, v, k, q, c.H, c.H, c.Hk, c.Hk, c.dv_, c.dk_, true, X,
+                             shared ? (void *)(c.ws + w.dq32) : c.dq, rdot};
+        const Roles<T> rk = {v, dy, q, nullptr, c.H, c.H, c.Hk, c.Hk, c.dv_, c.dk_, true, Y,
+                             shared ? (void *)(c.ws + w.dk32) : c.dk, nullptr};
+        const Roles<T> rv = {k, q, dy, v, c.Hk, c.Hk, c.H, c.H, c.dk_, c.dv_, false, Y, c.dv, cdot};
+        e = shared ? launch_grads<T, float>(c, geo, plan, rq, rk, rv) : launch_grads<T, T>(c, geo, plan, rq, rk, rv);
+        if (e == cudaSuccess && shared)
+            e = gdr_host::lin_group_sum(c, geo, w, (const float *)(c.ws + w.dq32), c.dq, c.dk_);
+        if (e == cudaSuccess && shared)
+            e = gdr_host::lin_group_sum(c, geo, w, (const float *)(c.ws + w.dk32), c.dk, c.dk_);
+        if (e != cudaSuccess) return e;
         gdr_host::ProfToken tk = gdr_host::prof_begin(GDR_K_LIN_GRAD, c.st);
         dg_kernel<<<dim3(geo.n_slots, c.H), kThreads, 0, c.st>>>(
             rdot, blocks_of(c.dk_), cdot, blocks_of(c.dv_), X, fin, Y, c.dg, part, geo, plan,

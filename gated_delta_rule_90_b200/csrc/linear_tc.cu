@@ -1414,7 +1414,8 @@ cudaError_t lin_fwd_tc(const LinCall &c) {
         s.gtot = (float *)(c.ws + w.gtot);
         if ((e = launch_chain<false, kStateOnly>(c, geo, plan, m.k, m.k, m.v, s, GDR_K_LIN_STATE)) != cudaSuccess)
             return e;
-        if ((e = lin_scan(c, geo, l, X, c.S0, nullptr, false)) != cudaSuccess) return e;
+        const LinScan f{X, s.gtot, c.S0, nullptr};
+        if ((e = lin_scan(c, geo, l, &f, nullptr)) != cudaSuccess) return e;
     }
     p.xin = c.S0;
     p.xblk = X;
@@ -1457,10 +1458,8 @@ cudaError_t lin_bwd_tc(const LinCall &c) {
         states_kernel<<<2 * n, kTcThreads, TcSmem<kStateOnly>::TOTAL, c.st>>>(m, s, t, n, geo, plan, c.err);
         prof_end(tk, c.st);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        if ((e = lin_scan(c, geo, l, X, c.S0, nullptr, false)) != cudaSuccess) return e;
-        LinWs back = l;
-        back.gtot = w.gtot_rev;
-        if ((e = lin_scan(c, geo, back, Y, c.dS_final, nullptr, true)) != cudaSuccess) return e;
+        const LinScan f{X, s.gtot, c.S0, nullptr}, b{Y, t.gtot, c.dS_final, nullptr};
+        if ((e = lin_scan(c, geo, l, &f, &b)) != cudaSuccess) return e;
     }
     // dq: (a, b, c) = (dout, v, k), the state transposed; beside it the pairs inside chunks
     TcArgs p{};
