@@ -343,12 +343,13 @@ def test_empty_calls(cuda_device):
     assert torch.equal(got[4], S0) and not got[3].any()
 
 
-def test_malformed_offsets_stay_in_bounds(cuda_device):
+@pytest.mark.parametrize("path,dtype", PATHS)
+def test_malformed_offsets_stay_in_bounds(cuda_device, path, dtype):
     """Offsets that decrease or leave [0, T] are taken as their running maximum inside [0, T]."""
-    x = inputs(cuda_device, 12, 1, 90, 2, 2, 32, 32, F32, "token", [0, 50, 20, 70, 500])
+    x = inputs(cuda_device, 12, 1, 90, 2, 2, 32, 32, dtype, "token", [0, 50, 20, 70, 500])
     y = dict(x, cu=[0, 50, 50, 70, 90])
     for call in (fwd, bwd):
-        assert all(torch.equal(a, b) for a, b in zip(call(x), call(y)))
+        assert all(torch.equal(a, b) for a, b in zip(call(x, path=path), call(y, path=path)))
 
 
 def test_refusals(cuda_device):
