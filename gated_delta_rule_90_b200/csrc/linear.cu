@@ -35,8 +35,9 @@ __device__ __forceinline__ int block_scan(int x, int *warp_tot, int *total) {
 // sequences never overlap and the slots always suffice.  `start` is scratch:
 // the sequences' first rows.
 __global__ void __launch_bounds__(1024)
-plan_kernel(const int32_t *__restrict__ cu, Geo geo, int4 *__restrict__ slot,
-            int *__restrict__ blk_start, int *__restrict__ start) {
+plan_kernel(const int32_t *cu, Geo geo, int4 *slot,
+            int *blk_start, int *start) {
+    stream_order();
     __shared__ int wt[32];
     const int tid = threadIdx.x;
     int hi = 0, nblk = 0;  // carried over tiles of 1024 sequences
@@ -126,6 +127,7 @@ __device__ __forceinline__ void scan(const ScanArgs &p, const Geo &geo, const Pl
 // forward in time (blockIdx.z below nf), then backward
 __global__ void __launch_bounds__(256)
 scan_kernel(ScanArgs f, ScanArgs r, int nf, Geo geo, Plan plan, int nel, unsigned int *err) {
+    stream_order();
     if ((int)blockIdx.z < nf)
         scan<false>(f, geo, plan, nel, err);
     else
@@ -138,7 +140,8 @@ scan_kernel(ScanArgs f, ScanArgs r, int nf, Geo geo, Plan plan, int nel, unsigne
 constexpr int kSumRows = 16;
 template <typename T>
 __global__ void __launch_bounds__(256)
-group_sum_kernel(const float *__restrict__ x, T *__restrict__ out, Geo geo, Plan plan, int d) {
+group_sum_kernel(const float *x, T *out, Geo geo, Plan plan, int d) {
+    stream_order();
     // slot by slot, so that rows of no sequence are left as they are
     const int4 sl = slot_of(geo, plan, blockIdx.x);
     const int r = geo.H / geo.Hk, per = geo.Hk * (d / 4);
@@ -162,7 +165,8 @@ group_sum_kernel(const float *__restrict__ x, T *__restrict__ out, Geo geo, Plan
 
 // GDR_GATE_HEAD: dg of a head from its slots' sums, in a fixed order, 64 bits.
 __global__ void __launch_bounds__(256)
-dg_heads_kernel(const float *__restrict__ part, float *__restrict__ dg, Geo geo) {
+dg_heads_kernel(const float *part, float *dg, Geo geo) {
+    stream_order();
     __shared__ double red[256];
     double s = 0.0;
     for (int i = threadIdx.x; i < geo.n_slots; i += 256) s += part[(size_t)i * geo.H + blockIdx.x];
@@ -363,9 +367,10 @@ cudaError_t lin_plan(const LinCall &c, const Geo &geo, const LinWs &w) {
     if (!geo.varlen) return cudaSuccess;
     int *bs = (int *)(c.ws + w.blk_start);
     ProfToken tk = prof_begin(GDR_K_LIN_PLAN, c.st);
-    plan_kernel<<<1, 1024, 0, c.st>>>(c.cu, geo, (int4 *)(c.ws + w.slot), bs, bs + geo.n_seq + 1);
+    const cudaError_t le = lin_launch(plan_kernel, dim3(1), 1024, 0, c.st, c.cu, geo, (int4 *)(c.ws + w.slot),
+                                      bs, bs + geo.n_seq + 1);
     prof_end(tk, c.st);
-    return cudaGetLastError();
+    return le;
 }
 
 cudaError_t lin_scan(const LinCall &c, const Geo &geo, const LinWs &w, const LinScan *f, const LinScan *r) {
@@ -377,9 +382,9 @@ cudaError_t lin_scan(const LinCall &c, const Geo &geo, const LinWs &w, const Lin
     if (f) a = {f->X, f->gtot, f->init, f->fin};
     if (r) b = {r->X, r->gtot, r->init, r->fin};
     ProfToken tk = prof_begin(GDR_K_LIN_SCAN, c.st);
-    scan_kernel<<<grid, 256, 0, c.st>>>(a, b, f ? 1 : 0, geo, plan, nel, c.err);
+    const cudaError_t le = lin_launch(scan_kernel, grid, 256, 0, c.st, a, b, f ? 1 : 0, geo, plan, nel, c.err);
     prof_end(tk, c.st);
-    return cudaGetLastError();
+    return le;
 }
 
 cudaError_t lin_group_sum(const LinCall &c, const Geo &geo, const LinWs &w, const float *x, void *out,
@@ -389,20 +394,20 @@ cudaError_t lin_group_sum(const LinCall &c, const Geo &geo, const LinWs &w, cons
     const int rounds = (geo.L + kSumRows - 1) / kSumRows;
     const dim3 grid(geo.n_slots, rounds < 4096 ? rounds : 4096);
     ProfToken tk = prof_begin(GDR_K_LIN_SUM, c.st);
-    if (c.dtype == GDR_BF16)
-        group_sum_kernel<__nv_bfloat16><<<grid, 256, 0, c.st>>>(x, (__nv_bfloat16 *)out, geo,
-                                                                       plan, d);
-    else
-        group_sum_kernel<float><<<grid, 256, 0, c.st>>>(x, (float *)out, geo, plan, d);
+    const cudaError_t le =
+        c.dtype == GDR_BF16
+            ? lin_launch(group_sum_kernel<__nv_bfloat16>, grid, 256, 0, c.st, x, (__nv_bfloat16 *)out, geo,
+                         plan, d)
+            : lin_launch(group_sum_kernel<float>, grid, 256, 0, c.st, x, (float *)out, geo, plan, d);
     prof_end(tk, c.st);
-    return cudaGetLastError();
+    return le;
 }
 
 cudaError_t lin_dg_heads(const LinCall &c, const Geo &geo, const float *part) {
     ProfToken tk = prof_begin(GDR_K_LIN_SUM, c.st);
-    dg_heads_kernel<<<c.H, 256, 0, c.st>>>(part, c.dg, geo);
+    const cudaError_t le = lin_launch(dg_heads_kernel, dim3(c.H), 256, 0, c.st, part, c.dg, geo);
     prof_end(tk, c.st);
-    return cudaGetLastError();
+    return le;
 }
 
 }  // namespace gdr_host

@@ -72,8 +72,8 @@ struct StateArgs {
     float *X;
 };
 template <typename T, bool REV>
-__device__ __forceinline__ void block_state(const StateArgs<T> &p, int z, const float *__restrict__ g,
-                                            float *__restrict__ gtot, const Geo &geo, const Plan &plan, int db,
+__device__ __forceinline__ void block_state(const StateArgs<T> &p, int z, const float *g,
+                                            float *gtot, const Geo &geo, const Plan &plan, int db,
                                             int dc, unsigned int *err) {
     const T *__restrict__ b = p.b, *__restrict__ c = p.c;
     float *__restrict__ X = p.X;
@@ -139,8 +139,9 @@ __device__ __forceinline__ void block_state(const StateArgs<T> &p, int z, const 
 // forward (blockIdx.z below nz), then reverse
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-state_kernel(StateArgs<T> f, StateArgs<T> r, int nz, const float *__restrict__ g, float *__restrict__ gtot,
+state_kernel(StateArgs<T> f, StateArgs<T> r, int nz, const float *g, float *gtot,
              Geo geo, Plan plan, int db, int dc, unsigned int *err) {
+    stream_order();
     const int z = blockIdx.z;
     if (z < nz)
         block_state<T, false>(f, z, g, gtot, geo, plan, db, dc, err);
@@ -161,7 +162,7 @@ struct Roles {
 };
 
 template <typename T, typename To, bool REV>
-__device__ __forceinline__ void outputs(const Roles<T> &ro, int z, const float *__restrict__ g, const Geo &geo,
+__device__ __forceinline__ void outputs(const Roles<T> &ro, int z, const float *g, const Geo &geo,
                                         const Plan &plan, unsigned int *err) {
     const float *__restrict__ X = ro.X;
     To *__restrict__ out = (To *)ro.out;
@@ -330,15 +331,17 @@ __device__ __forceinline__ void outputs(const Roles<T> &ro, int z, const float *
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-out_kernel(Roles<T> ro, const float *__restrict__ g, Geo geo, Plan plan, unsigned int *err) {
+out_kernel(Roles<T> ro, const float *g, Geo geo, Plan plan, unsigned int *err) {
+    stream_order();
     outputs<T, T, false>(ro, blockIdx.z, g, geo, plan, err);
 }
 // dq (blockIdx.z below nq), dk (below 2 nq), dv in one launch: a short step waited for each
 // (T 100, H 4, d 64: 55 us with a launch each, 38 us so and with states and carries in pairs)
 template <typename T, typename To>
 __global__ void __launch_bounds__(kThreads)
-grad_kernel(Roles<T> rq, Roles<T> rk, Roles<T> rv, int nq, const float *__restrict__ g, Geo geo, Plan plan,
+grad_kernel(Roles<T> rq, Roles<T> rk, Roles<T> rv, int nq, const float *g, Geo geo, Plan plan,
             unsigned int *err) {
+    stream_order();
     const int z = blockIdx.z;
     if (z < nq)
         outputs<T, To, false>(rq, z, g, geo, plan, err);
@@ -352,10 +355,11 @@ grad_kernel(Roles<T> rq, Roles<T> rk, Roles<T> rv, int nq, const float *__restri
 // One CTA per (slot, head): <S_end, dS_end>, then the reverse running sum of
 // R - C over the block's tokens, in 64 bits.
 __global__ void __launch_bounds__(kThreads)
-dg_kernel(const float *__restrict__ rdot, int nr, const float *__restrict__ cdot, int nc,
-          const float *__restrict__ X, const float *__restrict__ fin, const float *__restrict__ Y,
-          float *__restrict__ dg, float *__restrict__ part, Geo geo, Plan plan, int nel,
+dg_kernel(const float *rdot, int nr, const float *cdot, int nc,
+          const float *X, const float *fin, const float *Y,
+          float *dg, float *part, Geo geo, Plan plan, int nel,
           unsigned int *err) {
+    stream_order();
     __shared__ double red[kThreads / 32], suf[kThreads / 32];
     const int slot = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int4 sl = slot_of(geo, plan, slot);
@@ -445,10 +449,11 @@ cudaError_t launch_states(const gdr_host::LinCall &c, const Geo &geo, const Plan
     if (!geo.n_slots) return cudaSuccess;
     const int nz = blocks_of(c.dv_);
     gdr_host::ProfToken tk = gdr_host::prof_begin(GDR_K_LIN_STATE, c.st);
-    state_kernel<T><<<dim3(geo.n_slots, c.H, r ? 2 * nz : nz), kThreads, 0, c.st>>>(
-        f, r ? *r : f, nz, c.g, gtot, geo, plan, c.dk_, c.dv_, c.err);
+    const cudaError_t le = gdr_host::lin_launch(state_kernel<T>, dim3(geo.n_slots, c.H, r ? 2 * nz : nz),
+                                                kThreads, 0, c.st, f, r ? *r : f, nz, c.g, gtot, geo, plan,
+                                                c.dk_, c.dv_, c.err);
     gdr_host::prof_end(tk, c.st);
-    return cudaGetLastError();
+    return le;
 }
 
 template <typename T>
@@ -469,10 +474,10 @@ cudaError_t fwd_t(const gdr_host::LinCall &c) {
     static gdr_host::SmemLimit limit;
     if ((e = limit.set((const void *)out_kernel<T>, (int)out_smem(128))) != cudaSuccess) return e;
     gdr_host::ProfToken tk = gdr_host::prof_begin(GDR_K_LIN_OUT, c.st);
-    out_kernel<T><<<dim3(geo.n_slots, c.H, blocks_of(c.dv_)), kThreads, out_smem(c.dk_), c.st>>>(ro, c.g, geo, plan,
-                                                                                              c.err);
+    const cudaError_t le = gdr_host::lin_launch(out_kernel<T>, dim3(geo.n_slots, c.H, blocks_of(c.dv_)),
+                                                kThreads, out_smem(c.dk_), c.st, ro, c.g, geo, plan, c.err);
     gdr_host::prof_end(tk, c.st);
-    return cudaGetLastError();
+    return le;
 }
 
 template <typename T, typename To>
@@ -483,10 +488,12 @@ cudaError_t launch_grads(const gdr_host::LinCall &c, const Geo &geo, const Plan 
     if (e != cudaSuccess) return e;
     const int nq = blocks_of(c.dk_);
     gdr_host::ProfToken tk = gdr_host::prof_begin(GDR_K_LIN_GRAD, c.st);
-    grad_kernel<T, To><<<dim3(geo.n_slots, c.H, 2 * nq + blocks_of(c.dv_)), kThreads,
-                         out_smem(c.dk_ > c.dv_ ? c.dk_ : c.dv_), c.st>>>(rq, rk, rv, nq, c.g, geo, plan, c.err);
+    const cudaError_t le = gdr_host::lin_launch(grad_kernel<T, To>, dim3(geo.n_slots, c.H,
+                                                2 * nq + blocks_of(c.dv_)), kThreads,
+                                                out_smem(c.dk_ > c.dv_ ? c.dk_ : c.dv_), c.st, rq, rk, rv, nq,
+                                                c.g, geo, plan, c.err);
     gdr_host::prof_end(tk, c.st);
-    return cudaGetLastError();
+    return le;
 }
 
 template <typename T>
@@ -520,11 +527,11 @@ cudaError_t bwd_t(const gdr_host::LinCall &c) {
             e = gdr_host::lin_group_sum(c, geo, w, (const float *)(c.ws + w.dk32), c.dk, c.dk_);
         if (e != cudaSuccess) return e;
         gdr_host::ProfToken tk = gdr_host::prof_begin(GDR_K_LIN_GRAD, c.st);
-        dg_kernel<<<dim3(geo.n_slots, c.H), kThreads, 0, c.st>>>(
-            rdot, blocks_of(c.dk_), cdot, blocks_of(c.dv_), X, fin, Y, c.dg, part, geo, plan,
-            c.dk_ * c.dv_, c.err);
+        e = gdr_host::lin_launch(dg_kernel, dim3(geo.n_slots, c.H), kThreads, 0, c.st, rdot, blocks_of(c.dk_),
+                                 cdot, blocks_of(c.dv_), X, fin, Y, c.dg, part, geo, plan, c.dk_ * c.dv_,
+                                 c.err);
         gdr_host::prof_end(tk, c.st);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if (e != cudaSuccess) return e;
     }
     return part ? gdr_host::lin_dg_heads(c, geo, part) : cudaSuccess;
 }

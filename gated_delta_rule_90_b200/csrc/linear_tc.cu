@@ -210,11 +210,22 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// 16 bytes, asked for where this stands: a load that the compiler may move down to its
+// use costs the gradients of a batch 9 % (467 us, 427 so), and one of the read-only kind
+// may be moved above stream_order().
+__device__ __forceinline__ uint4 load_row4(const void *p) {
+    uint4 x;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                 : "l"(p));
+    return x;
+}
+
 // A log-decay, unclamped: a clamp where it is loaded would make the warp wait for
 // the load there (3300 cycles a chunk), not where the value is needed.
 __device__ __forceinline__ float load_raw_g(const Geo &geo, const float *g, long row, int h) {
     float x;
-    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(x) : "l"(geo.gate_head ? g + h : g + row * geo.H + h));
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(x) : "l"(geo.gate_head ? g + h : g + row * geo.H + h));
     return x;
 }
 
@@ -587,8 +598,9 @@ __device__ __forceinline__ void walk(unsigned int bid, const CUtensorMap &tm_a, 
                     const __nv_bfloat16 *e = p.e + (row * p.he + h / (geo.H / p.he)) * p.dc + c0 + 32 * hf;
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
-                        ev[u] = i < n && c0 + 32 * hf + 8 * u < p.dc ? __ldg(reinterpret_cast<const uint4 *>(e) + u)
-                                                                     : make_uint4(0, 0, 0, 0);
+                        ev[u] = i < n && c0 + 32 * hf + 8 * u < p.dc
+                                    ? load_row4(reinterpret_cast<const uint4 *>(e) + u)
+                                    : make_uint4(0, 0, 0, 0);
                 }
                 if (cc < nch) {
                     const float *tab = tabs + (cc & 1) * kTab;
@@ -1114,6 +1126,7 @@ template <bool REV, int MODE>
 __global__ void __launch_bounds__(kTcThreads, 1)
 chain_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
              const __grid_constant__ CUtensorMap tm_c, TcArgs p, Geo geo, Plan plan, unsigned int *err) {
+    stream_order();
     walk<REV, MODE>(blockIdx.x, tm_a, tm_b, tm_c, p, geo, plan, err);
 }
 struct Maps {
@@ -1126,6 +1139,7 @@ struct Maps {
 __global__ void __launch_bounds__(kTcThreads, 1)
 states_kernel(const __grid_constant__ Maps m, TcArgs p, TcArgs r, unsigned int n, Geo geo, Plan plan,
               unsigned int *err) {
+    stream_order();
     if (blockIdx.x < n)
         walk<false, kStateOnly>(blockIdx.x, m.k, m.k, m.v, p, geo, plan, err);
     else
@@ -1134,6 +1148,7 @@ states_kernel(const __grid_constant__ Maps m, TcArgs p, TcArgs r, unsigned int n
 __global__ void __launch_bounds__(kTcThreads, 1)
 dq_pairs_kernel(const __grid_constant__ Maps m, TcArgs p, PairArgs r, unsigned int n, Geo geo, Plan plan,
                 unsigned int *err) {
+    stream_order();
     if (blockIdx.x < n)
         walk<false, kOutDots>(blockIdx.x, m.o, m.v, m.k, p, geo, plan, err);
     else
@@ -1142,6 +1157,7 @@ dq_pairs_kernel(const __grid_constant__ Maps m, TcArgs p, PairArgs r, unsigned i
 __global__ void __launch_bounds__(kTcThreads, 1)
 dk_dv_kernel(const __grid_constant__ Maps m, TcArgs p, TcArgs r, unsigned int n, Geo geo, Plan plan,
              unsigned int *err) {
+    stream_order();
     if (blockIdx.x < n)
         walk<true, kOutDots>(blockIdx.x, m.v, m.o, m.q, p, geo, plan, err);
     else
@@ -1171,6 +1187,7 @@ __device__ __forceinline__ double warp_sum(double x) {
 
 __global__ void __launch_bounds__(kRun * kQ)
 dg_runs_kernel(DgArgs p, Geo geo, Plan plan) {
+    stream_order();
     constexpr int NW = kRun * kQ / 32;
     __shared__ double tot[NW], inter[NW], red[NW];
     const int slot = blockIdx.x / geo.H, h = blockIdx.x - slot * geo.H, run = blockIdx.y;
@@ -1383,9 +1400,10 @@ cudaError_t launch_chain(const LinCall &c, const Geo &geo, const Plan &plan, con
     if (e != cudaSuccess) return e;
     const unsigned int n = prepare(c, geo, &p);
     gdr_host::ProfToken tk = gdr_host::prof_begin(id, c.st);
-    chain_kernel<REV, MODE><<<n, kTcThreads, TcSmem<MODE>::TOTAL, c.st>>>(a, b, cc, p, geo, plan, c.err);
+    const cudaError_t le = gdr_host::lin_launch(chain_kernel<REV, MODE>, dim3(n), kTcThreads,
+                                                TcSmem<MODE>::TOTAL, c.st, a, b, cc, p, geo, plan, c.err);
     gdr_host::prof_end(tk, c.st);
-    return cudaGetLastError();
+    return le;
 }
 
 }  // namespace
@@ -1455,9 +1473,10 @@ cudaError_t lin_bwd_tc(const LinCall &c) {
         const unsigned int n = prepare(c, geo, &s);
         prepare(c, geo, &t);
         tk = prof_begin(GDR_K_LIN_STATE, c.st);
-        states_kernel<<<2 * n, kTcThreads, TcSmem<kStateOnly>::TOTAL, c.st>>>(m, s, t, n, geo, plan, c.err);
+        e = lin_launch(states_kernel, dim3(2 * n), kTcThreads, TcSmem<kStateOnly>::TOTAL, c.st, m, s, t, n, geo,
+                       plan, c.err);
         prof_end(tk, c.st);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if (e != cudaSuccess) return e;
         const LinScan f{X, s.gtot, c.S0, nullptr}, b{Y, t.gtot, c.dS_final, nullptr};
         if ((e = lin_scan(c, geo, l, &f, &b)) != cudaSuccess) return e;
     }
@@ -1491,10 +1510,10 @@ cudaError_t lin_bwd_tc(const LinCall &c) {
     if ((e = allow(&lim_q, dq_pairs_kernel)) != cudaSuccess) return e;
     unsigned int n = prepare(c, geo, &p);
     tk = prof_begin(GDR_K_LIN_GRAD, c.st);
-    dq_pairs_kernel<<<n + (unsigned)(units * split), kTcThreads, TcSmem<kOutDots>::TOTAL, c.st>>>(m, p, pa, n, geo,
-                                                                                               plan, c.err);
+    e = lin_launch(dq_pairs_kernel, dim3(n + (unsigned)(units * split)), kTcThreads, TcSmem<kOutDots>::TOTAL,
+                   c.st, m, p, pa, n, geo, plan, c.err);
     prof_end(tk, c.st);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (e != cudaSuccess) return e;
     // dk: (v, dout, q), backward in time
     p.xin = c.dS_final;
     p.xblk = Y;
@@ -1516,9 +1535,10 @@ cudaError_t lin_bwd_tc(const LinCall &c) {
     const unsigned int nv = prepare(c, geo, &r);
     static_assert(TcSmem<kOutDots>::TOTAL >= TcSmem<kOut>::TOTAL, "shared memory");
     tk = prof_begin(GDR_K_LIN_GRAD, c.st);
-    dk_dv_kernel<<<n + (over ? 0 : nv), kTcThreads, TcSmem<kOutDots>::TOTAL, c.st>>>(m, p, r, n, geo, plan, c.err);
+    e = lin_launch(dk_dv_kernel, dim3(n + (over ? 0 : nv)), kTcThreads, TcSmem<kOutDots>::TOTAL, c.st, m, p, r,
+                   n, geo, plan, c.err);
     prof_end(tk, c.st);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (e != cudaSuccess) return e;
     if (shared) {
         if ((e = lin_group_sum(c, geo, l, (const float *)(c.ws + w.dq32), c.dq, c.dk_)) != cudaSuccess) return e;
         if ((e = lin_group_sum(c, geo, l, (const float *)(c.ws + w.dk32), c.dk, c.dk_)) != cudaSuccess) return e;
@@ -1526,9 +1546,9 @@ cudaError_t lin_bwd_tc(const LinCall &c) {
     DgArgs d{ri, ci, rp, cp, (const float *)(c.ws + w.ydot), 2 * groups(c.dk_), 2 * groups(c.dk_),
              8 * groups(c.dk_), fin, c.dS_final, c.dg, part, c.dk_ * c.dv_, w.nbnd};
     tk = prof_begin(GDR_K_LIN_GRAD, c.st);
-    dg_runs_kernel<<<dim3((unsigned)units, (unsigned)w.nbnd), kRun * kQ, 0, c.st>>>(d, geo, plan);
+    e = lin_launch(dg_runs_kernel, dim3((unsigned)units, (unsigned)w.nbnd), kRun * kQ, 0, c.st, d, geo, plan);
     prof_end(tk, c.st);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (e != cudaSuccess) return e;
     if (part) {
         Geo by_run = geo;  // one sum per run and head
         by_run.n_slots = geo.n_slots * w.nbnd;

@@ -344,6 +344,59 @@ def test_empty_calls(cuda_device):
 
 
 @pytest.mark.parametrize("path,dtype", PATHS)
+def test_inputs_written_just_before_the_call(cuda_device, path, dtype):
+    """Kernels that end right before the calls, in the same stream or in one joined to it, write the
+    inputs; the gradients' inputs follow the forward pass.  Eager and captured: bit for bit the calls
+    on inputs that were ready."""
+    cu = [0, 300, 301, 900]
+    x, y = (inputs(cuda_device, 60 + i, 1, 900, 4, 2, 64, 64, dtype, "token", cu) for i in (0, 1))
+    want = [[t.clone() for t in fwd(z, path=path) + bwd(z, path=path)] for z in (x, y)]
+    ts = [n for n in x if isinstance(x[n], torch.Tensor) and n != "cu"]
+    live, src = dict(x), {n: x[n].clone() for n in ts}
+    for n in ts:
+        live[n] = torch.zeros_like(x[n])
+    c = torch.tensor(cu, dtype=torch.int32, device=cuda_device)
+    side = torch.cuda.Stream()
+
+    def step():
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            for n in ("k", "g"):
+                torch.mul(src[n], 1, out=live[n])
+        for n in ("v", "S0", "q"):
+            torch.mul(src[n], 1, out=live[n])
+        here.wait_stream(side)
+        o = binding.gdr_fwd_linear(live["q"], live["k"], live["v"], live["g"], live["S0"], cu_seqlens=c, path=path)
+        for n in ("dS", "dout"):
+            torch.mul(src[n], 1, out=live[n])
+        return o + binding.gdr_bwd_linear(live["q"], live["k"], live["v"], live["g"], live["dout"], live["S0"],
+                                          live["dS"], cu_seqlens=c, path=path)
+
+    def load(z):
+        for n in ts:
+            src[n].copy_(z[n])
+            live[n].zero_()
+        torch.cuda.synchronize()
+
+    for _ in range(10):
+        for z, w in zip((x, y), want):
+            load(z)
+            assert all(torch.equal(a, b) for a, b in zip(step(), w))
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        out = step()
+    for _ in range(10):
+        for z, w in zip((x, y), want):
+            load(z)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(out, w))
+    assert binding.device_status() == binding.GDR_OK
+
+
+@pytest.mark.parametrize("path,dtype", PATHS)
 def test_malformed_offsets_stay_in_bounds(cuda_device, path, dtype):
     """Offsets that decrease or leave [0, T] are taken as their running maximum inside [0, T]."""
     x = inputs(cuda_device, 12, 1, 90, 2, 2, 32, 32, dtype, "token", [0, 50, 20, 70, 500])
