@@ -426,6 +426,17 @@ def _linear_refuse(q, k, v, g):
             _linear_bad(dev, name, t, dtype, shape)
 
 
+def _linear_rank(axes, **tensors):
+    """Raise for tensors that do not have the ``axes`` of the call.  (Checked before anything is
+    read from a shape: tensors of another rank can agree with each other, and the counts taken
+    from their axes would then not be those of their memory.)"""
+    for name, t in tensors.items():
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dim() != axes:
+            raise ValueError(f"{name} has {t.dim()} axes; expected {axes}")
+
+
 def _linear_args(q, k, v, g, tensors):
     """Shapes and checks shared by the linear attention calls: q, k
     [*lead, H_k, d_k], v [*lead, H, d_v], g [*lead, H] or [H]; ``tensors`` are
@@ -507,6 +518,8 @@ def gdr_fwd_linear(q, k, v, g, S0=None, *, cu_seqlens=None, out=None, S_final=No
     [B,T,H_k,d_k], v [B,T,H,d_v] (value heads share query/key heads when
     H_k < H), g [B,T,H] or [H]; returns ``(out [B,T,H,d_v], S_final
     [N,H,d_v,d_k] or None)``."""
+    if len(q.shape) != 4 or len(v.shape) != 4:
+        _linear_rank(4, q=q, v=v)
     B, T = q.shape[:2]
     n_seq, varlen = _linear_cu(cu_seqlens, B)
     st_shape = (n_seq, v.shape[-2], v.shape[-1], q.shape[-1])
@@ -535,6 +548,8 @@ def gdr_decode_step_linear(q, k, v, g, S, *, out=None, stream=None) -> torch.Ten
     """Linear attention decode of one token per sequence, updating ``S``
     [N,H,d_v,d_k] in place: q, k [N,H_k,d_k], v [N,H,d_v], g [N,H] or [H];
     returns out [N,H,d_v]."""
+    if len(q.shape) != 3 or len(v.shape) != 3:
+        _linear_rank(3, q=q, v=v)
     N = q.shape[0]
     dev, dtype, gate, H, H_k, d_k, d_v = _linear_args(q, k, v, g, (
         ("S", S, torch.float32, (N, v.shape[-2], v.shape[-1], q.shape[-1])),
@@ -561,6 +576,8 @@ def gdr_bwd_linear(q, k, v, g, dout, S0=None, dS_final=None, *, cu_seqlens=None,
     """Gradients of gdr_fwd_linear from ``dout`` [B,T,H,d_v] and ``dS_final``
     [N,H,d_v,d_k] (None: zero); returns ``(dq, dk, dv, dg, dS0 or None)``,
     dq, dk and dv of the tokens' type, dg and dS0 fp32."""
+    if len(q.shape) != 4 or len(v.shape) != 4:
+        _linear_rank(4, q=q, v=v)
     B, T = q.shape[:2]
     n_seq, varlen = _linear_cu(cu_seqlens, B)
     st_shape = (n_seq, v.shape[-2], v.shape[-1], q.shape[-1])

@@ -1,0 +1,99 @@
+"""CPU checks of what the linear attention calls hand to the library: tensors
+that pass for CUDA ones, and a library that records its arguments instead of
+launching."""
+import pytest
+import torch
+
+from gated_delta_rule_90_b200 import binding
+
+F32 = torch.float32
+
+
+class OnGpu(torch.Tensor):
+    """A host tensor that says it is on cuda:0."""
+    __torch_function__ = torch._C._disabled_torch_function_impl
+    device = property(lambda self: torch.device("cuda:0"))
+    is_cuda = property(lambda self: True)
+
+    def get_device(self):
+        return 0
+
+
+class Library:
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            return binding.GDR_OK
+        return call
+
+
+@pytest.fixture
+def library(monkeypatch):
+    rec = Library()
+    monkeypatch.setattr(binding, "lib", lambda: rec)
+    monkeypatch.setattr(binding, "fwd_linear_workspace_size", lambda *a: 256)
+    monkeypatch.setattr(binding, "bwd_linear_workspace_size", lambda *a: 256)
+    monkeypatch.setattr(binding, "_linear_call", lambda dev, stream, n, ws, call: call(0, n, 0))
+    return rec
+
+
+def made(*shape):
+    return torch.zeros(*shape, dtype=F32).as_subclass(OnGpu)
+
+
+def tensors(lead, H=4, Hk=2, dk=32, dv=16):
+    return made(*lead, Hk, dk), made(*lead, Hk, dk), made(*lead, H, dv), made(*lead, H)
+
+
+def states(n, H=4, dk=32, dv=16):
+    return made(n, H, dv, dk)
+
+
+def fwd(lead, n):
+    q, k, v, g = tensors(lead)
+    return binding.gdr_fwd_linear(q, k, v, g, out=made(*v.shape), S_final=states(n))
+
+
+def bwd(lead, n):
+    q, k, v, g = tensors(lead)
+    return binding.gdr_bwd_linear(q, k, v, g, made(*v.shape), dq=made(*q.shape), dk=made(*q.shape),
+                                  dv=made(*v.shape), dg=made(*g.shape), dS0=states(n))
+
+
+def decode(lead, n):
+    q, k, v, g = tensors(lead)
+    return binding.gdr_decode_step_linear(q, k, v, g, states(n), out=made(*v.shape), stream=0)
+
+
+@pytest.mark.parametrize("call,lead,at,counts", [
+    (fwd, (3, 8), 7, (3, 8, 4, 2, 32, 16)), (bwd, (3, 8), 12, (3, 8, 4, 2, 32, 16)),
+    (decode, (3,), 6, (3, 4, 2, 32, 16))])
+def test_counts_that_reach_the_library(library, call, lead, at, counts):
+    call(lead, 3)
+    (_, args), = library.calls
+    assert args[at:at + len(counts)] == counts
+
+
+@pytest.mark.parametrize("call,lead", [
+    (fwd, (8,)), (fwd, (3, 8, 2)), (fwd, ()), (bwd, (8,)), (bwd, (3, 8, 2)), (bwd, ()),
+    (decode, ()), (decode, (3, 8)), (decode, (3, 1))])
+def test_tensors_of_another_rank_are_refused(library, call, lead):
+    """Unbatched tensors, a further axis, decode tensors with a token axis: each agrees with the
+    others in shape, and the library would read its counts from the wrong axes."""
+    with pytest.raises(ValueError, match="axes"):
+        call(lead, lead[0] if lead else 1)
+    assert not library.calls
+
+
+@pytest.mark.parametrize("name", ["k", "v", "g"])
+@pytest.mark.parametrize("call", [binding.gdr_fwd_linear, binding.gdr_decode_step_linear])
+def test_one_tensor_of_another_rank_is_refused(library, call, name):
+    lead = (3, 8) if call is binding.gdr_fwd_linear else (3,)
+    x = dict(zip("qkvg", tensors(lead)))
+    x[name] = x[name].reshape(1, *x[name].shape)
+    with pytest.raises(ValueError):
+        call(x["q"], x["k"], x["v"], x["g"], states(3))
+    assert not library.calls
