@@ -42,7 +42,7 @@ constexpr uint32_t kAtom = kQ * 128;     // bytes of 128 rows of 64 bf16
 constexpr float kLog2e = 1.4426950408889634f;
 
 enum { kStateOnly = 0, kOut = 1, kOutDots = 2 };
-constexpr int kRun = 4;  // chunks over which the gradient of the decays is summed before it starts again
+constexpr int kRun = kRunLen / kQ;  // chunks of a run
 
 // Tables of a chunk's decays (floats): LC sums inside each 32-token block in
 // units of log 2, CF column factors, then scalars by block (see decay_tables).
@@ -91,10 +91,9 @@ struct TcArgs {
     void *out;           // bf16, or fp32 with out32
     const __nv_bfloat16 *e;  // dots: rows that the state's part of out is multiplied with
     float *dots;         // [2 x column groups, rows, H]
-    // dots, forward: the state where every kRun-th chunk of a block starts, as the state's threads
-    // hold it; reverse: its products with the gradient of that state, by warp
+    // dots, forward: the state where a run starts, as the state's threads hold it; reverse: its
+    // products with the gradient of that state, by warp
     float *bnd, *ydot;
-    int nbnd;            // of a block
     int ha, hb, hc, he;  // heads of a, b, c, e
     int db, dc, ng;      // widths, column groups
     int tr;              // states are stored as the transpose of X
@@ -358,7 +357,9 @@ __device__ __forceinline__ void walk(unsigned int bid, const CUtensorMap &tm_a, 
     if (MODE == kStateOnly && last) return;
     if (kChecked && !(chk_span(t0, len, geo.rows, err) && chk_span(slot, 1, geo.n_slots, err) &&
                       chk_tma(c0, 0, 2, p.dc, 1, err) &&
-                      chk_true((smem_u32(sm) & 1023u) == 0 && len <= geo.L, err)))
+                      chk_true((smem_u32(sm) & 1023u) == 0 && len <= geo.L, err) &&
+                      (MODE != kOutDots || chk_span(run_of(geo, t0, slot), (len + kRunLen - 1) / kRunLen,
+                                                    geo.n_runs, err))))
         return;
 
     if (tid == 0) {
@@ -840,18 +841,16 @@ __device__ __forceinline__ void walk(unsigned int bid, const CUtensorMap &tm_a, 
                 if (update && cc < nch && MODE != kStateOnly) {
                     if (MODE == kOutDots) {
                         const int e = nch - cc;  // reverse: the chunk whose start this is
-                        int at = -1;             // boundary: block, and start of the block's chunk at * kRun
-                        int bs = slot;
+                        int at = -1;             // the run that starts there; at the block's end the next block's first
                         if (!REV) {
-                            if (cc % kRun == 0) at = cc / kRun;
+                            if (cc % kRun == 0) at = run_of(geo, t0, slot) + cc / kRun;
                         } else if (cc > 0) {
-                            if (e % kRun == 0) at = e / kRun;
+                            if (e % kRun == 0) at = run_of(geo, t0, slot) + e / kRun;
                         } else if (sl.w < nblk - 1) {
-                            bs = slot + 1;
-                            at = 0;
+                            at = run_of(geo, t0 + len, slot + 1);
                         }
                         if (at >= 0) {
-                            const size_t u = (((size_t)bs * p.nbnd + at) * geo.H + h) * p.ng + ng;
+                            const size_t u = ((size_t)at * geo.H + h) * p.ng + ng;
                             float4 *b4 = reinterpret_cast<float4 *>(p.bnd) + u * (8 * 256) + (tid - 256);
                             if (!REV) {
 #pragma unroll
@@ -1177,7 +1176,7 @@ struct DgArgs {
     int nri, nci, ny;           // planes of ri, ci; products of a boundary
     const float *fin, *dfin;    // S, dS at the sequences' ends, or dfin NULL (zero)
     float *dg, *part;
-    int nel, nbnd;
+    int nel;
 };
 __device__ __forceinline__ double warp_sum(double x) {
 #pragma unroll
@@ -1185,29 +1184,31 @@ __device__ __forceinline__ double warp_sum(double x) {
     return x;
 }
 
-__global__ void __launch_bounds__(kRun * kQ)
+__global__ void __launch_bounds__(kRunLen)
 dg_runs_kernel(DgArgs p, Geo geo, Plan plan) {
     stream_order();
-    constexpr int NW = kRun * kQ / 32;
+    constexpr int NW = kRunLen / 32;
     __shared__ double tot[NW], inter[NW], red[NW];
-    const int slot = blockIdx.x / geo.H, h = blockIdx.x - slot * geo.H, run = blockIdx.y;
+    const int no = blockIdx.x / geo.H, h = blockIdx.x - no * geo.H;  // number of the run
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, grp = tid / kQ;
-    const int4 sl = slot_of(geo, plan, slot);
-    const int first = run * kRun * kQ, len = sl.y - first;  // tokens from the run's start
+    const int2 at_run = geo.varlen ? plan.run[no] : make_int2(no / geo.nrun, no % geo.nrun);
+    const int slot = at_run.x;
+    const int4 sl = slot < 0 ? make_int4(0, -1, 0, 0) : slot_of(geo, plan, slot);
+    const int first = at_run.y * kRunLen, len = sl.y - first;  // tokens from the run's start
     if (len <= 0) {
-        if (p.part && tid == 0) p.part[((size_t)slot * p.nbnd + run) * geo.H + h] = 0.f;
+        if (p.part && tid == 0) p.part[(size_t)no * geo.H + h] = 0.f;
         return;
     }
     const int nblk = geo.varlen ? plan.blk_start[sl.z + 1] - plan.blk_start[sl.z] : geo.nb;
-    const bool more = len > kRun * kQ;  // the block goes on after the run
+    const bool more = len > kRunLen;  // the block goes on after the run
     double f = 0.0;
     if (more || sl.w < nblk - 1) {
-        const size_t u = ((size_t)(more ? slot : slot + 1) * p.nbnd + (more ? run + 1 : 0)) * geo.H + h;
+        const size_t u = (size_t)(more ? no + 1 : run_of(geo, sl.x + sl.y, slot + 1)) * geo.H + h;
         if (tid < p.ny) f = p.ydot[u * p.ny + tid];
     } else if (p.dfin) {
         const size_t o = ((size_t)sl.z * geo.H + h) * p.nel;
         float acc = 0.f;
-        for (int i = tid; i < p.nel / 4; i += kRun * kQ) {
+        for (int i = tid; i < p.nel / 4; i += kRunLen) {
             const float4 a = reinterpret_cast<const float4 *>(p.fin + o)[i];
             const float4 b = reinterpret_cast<const float4 *>(p.dfin + o)[i];
             acc = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, acc))));
@@ -1253,7 +1254,7 @@ dg_runs_kernel(DgArgs p, Geo geo, Plan plan) {
     __syncthreads();
     if (warp == 0) {
         x = warp_sum(lane < NW ? red[lane] : 0.0);
-        if (lane == 0) p.part[((size_t)slot * p.nbnd + run) * geo.H + h] = (float)x;
+        if (lane == 0) p.part[(size_t)no * geo.H + h] = (float)x;
     }
 }
 
@@ -1306,8 +1307,8 @@ int block_len(int n_seq, bool varlen, bool bwd, int T, int H, int ng, size_t nel
 }
 
 struct TcWs {
-    size_t slot, blk_start, gtot, gtot_rev, X, Y, fin, ri, ci, rp, cp, bnd, ydot, dq32, dk32, part, total;
-    int L, nb, n_slots, multi, nbnd;
+    size_t slot, blk_start, run, gtot, gtot_rev, X, Y, fin, ri, ci, rp, cp, bnd, ydot, dq32, dk32, part, total;
+    int L, nb, n_slots, multi, nrun, n_runs;
 };
 TcWs tc_ws(const LinCall &c, bool bwd) {
     TcWs w{};
@@ -1320,7 +1321,8 @@ TcWs tc_ws(const LinCall &c, bool bwd) {
     w.nb = (c.T + w.L - 1) / w.L;
     w.n_slots = varlen ? c.T / w.L + n_seq : c.B * w.nb;
     w.multi = w.nb > 1;
-    w.nbnd = (w.L + kRun * kQ - 1) / (kRun * kQ);
+    w.nrun = (w.L + kRunLen - 1) / kRunLen;
+    w.n_runs = !bwd ? 0 : varlen ? c.T / kRunLen + w.n_slots : w.n_slots * w.nrun;  // run_of
     const size_t sh = (size_t)w.n_slots * c.H;
     size_t o = 0;
     auto take = [&](size_t bytes) {
@@ -1330,6 +1332,7 @@ TcWs tc_ws(const LinCall &c, bool bwd) {
     };
     w.slot = take(varlen ? sizeof(int4) * w.n_slots : 0);
     w.blk_start = take(varlen ? sizeof(int) * ((size_t)3 * n_seq + 1) : 0);
+    w.run = take(varlen ? sizeof(int2) * w.n_runs : 0);
     w.gtot = take(w.multi ? sh * 4 : 0);
     w.gtot_rev = take(bwd && w.multi ? sh * 4 : 0);
     w.X = take(w.multi ? sh * nel * 4 : 0);
@@ -1342,9 +1345,10 @@ TcWs tc_ws(const LinCall &c, bool bwd) {
         w.cp = take(rows * c.H * 2 * 4);
         w.dq32 = take(c.Hk < c.H ? rows * c.H * c.dk_ * 4 : 0);
         w.dk32 = take(c.Hk < c.H ? rows * c.H * c.dk_ * 4 : 0);
-        w.bnd = take(sh * w.nbnd * gk * kN * 128 * 4);
-        w.ydot = take(sh * w.nbnd * gk * 8 * 4);
-        w.part = take(sh * w.nbnd * 4);
+        const size_t runs = (size_t)w.n_runs * c.H;
+        w.bnd = take(runs * gk * kN * 128 * 4);
+        w.ydot = take(runs * gk * 8 * 4);
+        w.part = take(runs * 4);
     }
     w.total = o ? o : 256;  // 0 stands for a refused call
     return w;
@@ -1354,6 +1358,9 @@ gdr_host::LinWs common_ws(const TcWs &w) {
     gdr_host::LinWs l{};
     l.slot = w.slot;
     l.blk_start = w.blk_start;
+    l.run = w.run;
+    l.nrun = w.nrun;
+    l.n_runs = w.n_runs;
     l.gtot = w.gtot;
     l.n_slots = w.n_slots;
     l.nb = w.nb;
@@ -1417,7 +1424,7 @@ cudaError_t lin_fwd_tc(const LinCall &c) {
     const LinWs l = common_ws(w);
     Geo geo = lin_geo(c, l);
     geo.keep_empty = geo.skip_single = 1;
-    const Plan plan = {(const int4 *)(c.ws + w.slot), (const int *)(c.ws + w.blk_start)};
+    const Plan plan = {(const int4 *)(c.ws + w.slot), (const int *)(c.ws + w.blk_start), (const int2 *)(c.ws + w.run)};
     Maps m;
     if (!make_maps(&m, c)) return cudaErrorUnknown;
     cudaError_t e;
@@ -1447,7 +1454,7 @@ cudaError_t lin_bwd_tc(const LinCall &c) {
     const LinWs l = common_ws(w);
     Geo geo = lin_geo(c, l);
     geo.keep_empty = geo.skip_single = 1;
-    const Plan plan = {(const int4 *)(c.ws + w.slot), (const int *)(c.ws + w.blk_start)};
+    const Plan plan = {(const int4 *)(c.ws + w.slot), (const int *)(c.ws + w.blk_start), (const int2 *)(c.ws + w.run)};
     Maps m;
     if (!make_maps(&m, c)) return cudaErrorUnknown;
     cudaError_t e;
@@ -1493,7 +1500,6 @@ cudaError_t lin_bwd_tc(const LinCall &c) {
     p.dots = ri;
     p.bnd = (float *)(c.ws + w.bnd);
     p.ydot = (float *)(c.ws + w.ydot);
-    p.nbnd = w.nbnd;
     // pairs: CTAs for a (slot, head), as many as end soonest on 148 SMs, a start costing about as
     // much as one and a half chunks (B4 T4096 H16 d128: two, 191 us with dq's walks; four 200)
     const long units = (long)geo.n_slots * geo.H, most = w.L / kQ;
@@ -1544,14 +1550,14 @@ cudaError_t lin_bwd_tc(const LinCall &c) {
         if ((e = lin_group_sum(c, geo, l, (const float *)(c.ws + w.dk32), c.dk, c.dk_)) != cudaSuccess) return e;
     }
     DgArgs d{ri, ci, rp, cp, (const float *)(c.ws + w.ydot), 2 * groups(c.dk_), 2 * groups(c.dk_),
-             8 * groups(c.dk_), fin, c.dS_final, c.dg, part, c.dk_ * c.dv_, w.nbnd};
+             8 * groups(c.dk_), fin, c.dS_final, c.dg, part, c.dk_ * c.dv_};
     tk = prof_begin(GDR_K_LIN_GRAD, c.st);
-    e = lin_launch(dg_runs_kernel, dim3((unsigned)units, (unsigned)w.nbnd), kRun * kQ, 0, c.st, d, geo, plan);
+    e = lin_launch(dg_runs_kernel, dim3((unsigned)geo.n_runs * geo.H), kRunLen, 0, c.st, d, geo, plan);
     prof_end(tk, c.st);
     if (e != cudaSuccess) return e;
     if (part) {
         Geo by_run = geo;  // one sum per run and head
-        by_run.n_slots = geo.n_slots * w.nbnd;
+        by_run.n_slots = geo.n_runs;
         if ((e = lin_dg_heads(c, by_run, part)) != cudaSuccess) return e;
     }
     return over ? launch_chain<true, kOut>(c, geo, plan, m.k, m.q, m.o, r, GDR_K_LIN_GRAD) : cudaSuccess;

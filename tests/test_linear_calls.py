@@ -97,3 +97,22 @@ def test_one_tensor_of_another_rank_is_refused(library, call, name):
     with pytest.raises(ValueError):
         call(x["q"], x["k"], x["v"], x["g"], states(3))
     assert not library.calls
+
+
+@pytest.mark.parametrize("H,Hk,dk,dv", [(16, 16, 128, 128), (32, 8, 128, 64), (4, 4, 64, 64), (2, 1, 48, 112)])
+@pytest.mark.parametrize("T", [2048, 65536, 131072])
+def test_workspace_of_packed_gradients_is_linear_in_the_sequences(H, Hk, dk, dv, T):
+    """A further sequence adds at most its own part: for each head the states of its block, forward
+    and backward, and its last state (fp32, d_v x d_k), the state at one run's start (128 x 64 fp32
+    for each 64 columns of d_k) with 8 partial products, a few words of its plan, and the rounding
+    of the arrays to 256 bytes."""
+    groups = -(-dk // 64)
+    a = H * (3 * dk * dv * 4 + groups * (128 * 64 * 4 + 8 * 4) + 64) + 64
+
+    def size(n):
+        return binding.bwd_linear_workspace_size(1, T, H, Hk, dk, dv, n, True, binding.GDR_BF16,
+                                                 binding.GDR_GATE_HEAD, "tc")
+
+    base = size(1)
+    for n in (2, 16, 256, 2000):
+        assert base < size(n) <= base + (n - 1) * a + 20 * 256
