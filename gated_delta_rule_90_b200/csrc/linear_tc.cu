@@ -45,8 +45,9 @@ enum { kStateOnly = 0, kOut = 1, kOutDots = 2 };
 constexpr int kRun = kRunLen / kQ;  // chunks of a run
 
 // Tables of a chunk's decays (floats): LC sums inside each 32-token block in
-// units of log 2, CF column factors, then scalars by block (see decay_tables).
-enum { kLC = 0, kCF = 128, kSS = 256, kSE = 260, kBB = 264, kDEC = 270, kLE = 272, kTab = 276 };
+// units of log 2, CF column factors, then scalars by block (see decay_tables); for
+// the pairs also LL, what LC leaves of its sums.
+enum { kLC = 0, kCF = 128, kSS = 256, kSE = 260, kBB = 264, kDEC = 270, kTab = 272, kLL = 272, kPairTab = 400 };
 
 // Shared memory of a CTA.  Two buffers of each tile, the three terms of w C, and
 // X in one term; where X takes three, a has one buffer (it is free early: its two
@@ -244,6 +245,7 @@ __device__ __forceinline__ Two add(const Two &a, const Two &b) {
     const float l = s.l + (a.l + b.l), h = s.h + l;
     return {h, l - (h - s.h)};
 }
+__device__ __forceinline__ Two sub(const Two &a, const Two &b) { return add(a, {-b.h, -b.l}); }
 __device__ __forceinline__ float diff(const Two &a, const Two &b) {
     const Two s = two_sum(a.h, -b.h);
     return s.h + (s.l + (a.l - b.l));
@@ -260,7 +262,13 @@ __device__ __forceinline__ Two shfl(const Two &a, int lane) {
 //   pair in one block: 2^(difference of LC);
 //   w_j = column factor(j) SE or SS(block), the state's weight = row factor(i) SS or SE,
 // SS_b = e^{s_b}, SE_b = e^{G_n - e_b}, BB = e^{s_later - e_earlier}.  Returns G_n.
-template <bool REV>
+// LC is taken from the border of the row factor, s forward and e reverse, so that this
+// factor is the power of a sum rounded once, at its own size.  A difference of two LC is
+// rounded at the size of the sums: after decays of 0 earlier in the block (-104 each, 32 of
+// them at most) by up to 2^-12, less than the rounding of P to bf16 (2^-8), which is all
+// that the walks use it for.  The pairs, whose sums are fp32, need LL as well (their dg was
+// off by 8.5e-5 of its norm where every 4th decay was 0, by 3.5e-7 so).
+template <bool REV, bool LOW = false>
 __device__ __forceinline__ Two decay_tables(float *tab, const float (&gv)[4], int lane) {
     Two p[4];
     p[0] = {gv[0], 0.f};
@@ -283,16 +291,19 @@ __device__ __forceinline__ Two decay_tables(float *tab, const float (&gv)[4], in
     };
     const int kb = lane >> 3;
     const Two s0 = border(kb), s1 = border(kb + 1);
-    float lc[4], cf[4];
+    float lc[4], ll[4], cf[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
         const Two G = add(base, p[u]);
-        lc[u] = diff(G, s0) * kLog2e;
+        const Two L = sub(G, REV ? s1 : s0);
+        lc[u] = L.h * kLog2e;
+        ll[u] = fmaf(L.h, kLog2e, -lc[u]) + L.l * kLog2e;
         cf[u] = expf(REV ? diff(G, s0) : diff(s1, G));
     }
     reinterpret_cast<float4 *>(tab + kLC)[lane] = make_float4(lc[0], lc[1], lc[2], lc[3]);
+    if (LOW) reinterpret_cast<float4 *>(tab + kLL)[lane] = make_float4(ll[0], ll[1], ll[2], ll[3]);
     reinterpret_cast<float4 *>(tab + kCF)[lane] = make_float4(cf[0], cf[1], cf[2], cf[3]);
-    // lanes 0-3 SS, 4-7 SE, 8-13 BB (pairs 10 20 21 30 31 32), 14 DEC, 16-19 LE
+    // lanes 0-3 SS, 4-7 SE, 8-13 BB (pairs 10 20 21 30 31 32), 14 DEC
     int hi = lane & 3, lo = 0;
     if (lane >= 4 && lane < 8) { hi = 4; lo = lane - 3; }
     if (lane >= 8 && lane < 14) {
@@ -300,16 +311,14 @@ __device__ __forceinline__ Two decay_tables(float *tab, const float (&gv)[4], in
         lo = lane - 8 - hi * (hi - 1) / 2 + 1;
     }
     if (lane == 14) hi = 4;
-    if (lane >= 16) { lo = lane & 3; hi = lo + 1; }
     const Two bh = border(hi), bl = border(lo);
-    const float d = diff(bh, bl);
-    if (lane < 15 || (lane >= 16 && lane < 20)) tab[kSS + lane] = lane < 15 ? expf(d) : d * kLog2e;
+    if (lane < 15) tab[kSS + lane] = expf(diff(bh, bl));
     return Gn;
 }
-// row factor of row i (block rb) from its LC
+// row factor of a row from its LC
 template <bool REV>
-__device__ __forceinline__ float row_factor(const float *tab, int rb, float li) {
-    return exp2f(REV ? tab[kLE + rb] - li : li);
+__device__ __forceinline__ float row_factor(float li) {
+    return exp2f(REV ? -li : li);
 }
 
 // Roles of the 20 warps: 8 of outputs, 8 of the state; the decays; TMA with the MMAs
@@ -609,7 +618,7 @@ __device__ __forceinline__ void walk(unsigned int bid, const CUtensorMap &tm_a, 
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc_fence_after();
-                    const float li = tab[kLC + i], rf = row_factor<REV>(tab, rb, li);
+                    const float li = tab[kLC + i], rf = row_factor<REV>(li);
                     egn = rf * tab[(REV ? kSE : kSS) + rb];
                     // weights of the pairs: this half's 16 columns of each block
 #pragma unroll 1
@@ -935,7 +944,7 @@ struct PairArgs {
 };
 struct PairSmem {
     static constexpr uint32_t QK = 0, VO = 4 * kAtom, TAB = 8 * kAtom;
-    static constexpr uint32_t BARS = TAB + 2 * kTab * 4, TOTAL = BARS + 8 * 8 + 16;
+    static constexpr uint32_t BARS = TAB + 2 * kPairTab * 4, TOTAL = BARS + 8 * 8 + 16;
 };
 
 __device__ __forceinline__ void pairs(unsigned int bid, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
@@ -1041,11 +1050,11 @@ __device__ __forceinline__ void pairs(unsigned int bid, const CUtensorMap &tm_q,
             if (it) ok = wait(tfree, (it - 1) & 1, err);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            float *tab = reinterpret_cast<float *>(sm + PairSmem::TAB) + (warp - 2) * kTab;
+            float *tab = reinterpret_cast<float *>(sm + PairSmem::TAB) + (warp - 2) * kPairTab;
             if (warp == 2)
-                decay_tables<false>(tab, gv, lane);
+                decay_tables<false, true>(tab, gv, lane);
             else
-                decay_tables<true>(tab, gv, lane);
+                decay_tables<true, true>(tab, gv, lane);
             __syncwarp();
             if (lane == 0) mbar_arrive(tfull);
             if (cc + p.split < nch) load(cc + p.split);
@@ -1055,7 +1064,7 @@ __device__ __forceinline__ void pairs(unsigned int bid, const CUtensorMap &tm_q,
         const bool rev = warp >= 12;
         const int rb = warp & 3, hf = ((warp - 4) >> 2) & 1, i = rb * 32 + lane;
         const uint32_t lb = (uint32_t)(rb * 32) << 16, col = rev ? 128 : 0;
-        const float *tab = reinterpret_cast<const float *>(sm + PairSmem::TAB) + (rev ? kTab : 0);
+        const float *tab = reinterpret_cast<const float *>(sm + PairSmem::TAB) + (rev ? kPairTab : 0);
         int it = 0;
         for (int cc = first; cc < nch; cc += p.split, ++it) {
             const int n = min(kQ, len - cc * kQ);
@@ -1065,8 +1074,8 @@ __device__ __forceinline__ void pairs(unsigned int bid, const CUtensorMap &tm_q,
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
-            const float li = tab[kLC + i];
-            const float rf = rev ? row_factor<true>(tab, rb, li) : row_factor<false>(tab, rb, li);
+            const float li = tab[kLC + i], ll = tab[kLL + i];
+            const float rf = rev ? row_factor<true>(li) : row_factor<false>(li);
             float s = 0.f;
 #pragma unroll 1
             for (int b = rev ? rb : 0; b <= (rev ? 3 : rb); ++b) {
@@ -1083,12 +1092,23 @@ __device__ __forceinline__ void pairs(unsigned int bid, const CUtensorMap &tm_q,
                 float r0 = 0.f, r1 = 0.f;
 #pragma unroll
                 for (int u = 0; u < 16; u += 2) mul2(x[u], x[u + 1], y[u], y[u + 1]);
+                if (b == rb) {
+#pragma unroll
+                    for (int u = 0; u < 16; u += 4) {
+                        const float4 l = *reinterpret_cast<const float4 *>(tab + kLL + c + u);
+                        const float d[4] = {l.x - ll, l.y - ll, l.z - ll, l.w - ll};
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            const float e = (f[u + w] - li) + d[w];
+                            f[u + w] = ex2(rev ? e : -e);
+                        }
+                    }
+                }
                 if (b == rb || c + 16 > n) {  // selects: what lies outside cannot matter
 #pragma unroll
                     for (int u = 0; u < 16; ++u) {
                         const int at = u + 16 * hf;
                         const bool in = c + u < n && (b != rb || (rev ? at > lane : at < lane));
-                        if (b == rb) f[u] = ex2(rev ? f[u] - li : li - f[u]);
                         x[u] = in ? x[u] * f[u] : 0.f;
                     }
 #pragma unroll
