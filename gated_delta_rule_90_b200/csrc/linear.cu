@@ -298,6 +298,10 @@ gdr_status resolve(int T, gdr_dtype dtype, gdr_path path, bool *tc) {
     return path == GDR_PATH_TENSORCORE && dtype != GDR_BF16 ? GDR_ERR_UNSUPPORTED : GDR_OK;
 }
 
+// What the size functions answer: 0 stands for a refused call, so a call of no tokens is given
+// a size as well, though it takes NULL.
+size_t ask(size_t need) { return need ? need : 256; }
+
 template <typename T, int VPL, int LPR>
 cudaError_t launch_decode(const LinCall &c) {
     // Rows of a head go to several CTAs while there are few heads: one CTA
@@ -428,7 +432,7 @@ size_t gdr_fwd_linear_workspace_size(int B, int T, int H, int H_k, int d_k, int 
     static const int32_t packed = 0;  // only whether cu is NULL matters here
     c.cu = varlen ? &packed : nullptr;
     c.B = B; c.T = T; c.H = H; c.Hk = H_k; c.dk_ = d_k; c.dv_ = d_v; c.n_seq = n_seq;
-    return tc ? gdr_host::lin_tc_ws_bytes(c, false) : gdr_host::lin_simt_ws_bytes(c, false);
+    return ask(tc ? gdr_host::lin_tc_ws_bytes(c, false) : gdr_host::lin_simt_ws_bytes(c, false));
 }
 
 size_t gdr_bwd_linear_workspace_size(int B, int T, int H, int H_k, int d_k, int d_v, int n_seq,
@@ -441,7 +445,7 @@ size_t gdr_bwd_linear_workspace_size(int B, int T, int H, int H_k, int d_k, int 
     static const int32_t packed = 0;
     c.cu = varlen ? &packed : nullptr;
     c.B = B; c.T = T; c.H = H; c.Hk = H_k; c.dk_ = d_k; c.dv_ = d_v; c.n_seq = n_seq;
-    return tc ? gdr_host::lin_tc_ws_bytes(c, true) : gdr_host::lin_simt_ws_bytes(c, true);
+    return ask(tc ? gdr_host::lin_tc_ws_bytes(c, true) : gdr_host::lin_simt_ws_bytes(c, true));
 }
 
 gdr_status gdr_fwd_linear(const void *q, const void *k, const void *v, const float *g,

@@ -265,7 +265,7 @@ __device__ __forceinline__ Two shfl(const Two &a, int lane) {
 // LC is taken from the border of the row factor, s forward and e reverse, so that this
 // factor is the power of a sum rounded once, at its own size.  A difference of two LC is
 // rounded at the size of the sums: after decays of 0 earlier in the block (-104 each, 32 of
-// them at most) by up to 2^-12, less than the rounding of P to bf16 (2^-8), which is all
+// them at most) by up to 2^-11, less than the rounding of P to bf16 (2^-8), which is all
 // that the walks use it for.  The pairs, whose sums are fp32, need LL as well (their dg was
 // off by 8.5e-5 of its norm where every 4th decay was 0, by 3.5e-7 so).
 template <bool REV, bool LOW = false>

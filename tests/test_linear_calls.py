@@ -116,3 +116,30 @@ def test_workspace_of_packed_gradients_is_linear_in_the_sequences(H, Hk, dk, dv,
     base = size(1)
     for n in (2, 16, 256, 2000):
         assert base < size(n) <= base + (n - 1) * a + 20 * 256
+
+
+@pytest.mark.parametrize("dtype", [binding.GDR_F32, binding.GDR_BF16])
+@pytest.mark.parametrize("gate", [binding.GDR_GATE_SCALAR, binding.GDR_GATE_HEAD])
+@pytest.mark.parametrize("varlen", [False, True])
+def test_a_call_without_tokens_has_a_workspace_size(dtype, gate, varlen):
+    """0 stands for a refused call; a call of no tokens is a valid one."""
+    a = (1 if varlen else 2, 0, 3, 1, 32, 16, 2, varlen, dtype, gate)
+    assert binding.fwd_linear_workspace_size(*a) > 0
+    assert binding.bwd_linear_workspace_size(*a) > 0
+
+
+@pytest.mark.parametrize("dtype,path,block", [(binding.GDR_F32, "simt", 32), (binding.GDR_BF16, "simt", 32),
+                                              (binding.GDR_BF16, "tc", 128)])
+@pytest.mark.parametrize("B,T,H,Hk", [(1, 640, 16, 8), (2, 4096, 16, 16), (4, 1000, 64, 4), (1, 65536, 32, 32)])
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 128), (16, 48)])
+def test_workspace_of_equal_sequences_is_bounded(dtype, path, block, B, T, H, Hk, dk, dv):
+    """At the shortest blocks: a state for each block and head; of the gradients two, with the state
+    (128 x 64 for each 64 columns) and 8 products at a run's start, the last states, four fp32 rows of
+    partial sums for dq and for dk each and two more of the pairs, and fp32 dq and dk where value heads
+    share them; words for each block, and 16 roundings to 256 bytes."""
+    blocks, rows, nel, groups = B * -(-T // block) * H, B * T * H, dk * dv, -(-dk // 64)
+    a = (B, T, H, Hk, dk, dv, 0, False, dtype, binding.GDR_GATE_SCALAR, path)
+    assert 0 < binding.fwd_linear_workspace_size(*a) <= blocks * (4 * nel + 16) + 16 * 256
+    most = blocks * (8 * nel + groups * (128 * 64 * 4 + 32) + 16) + B * H * nel * 4 + rows * (2 * 16 + 16)
+    most += rows * dk * 8 if Hk < H else 0
+    assert 0 < binding.bwd_linear_workspace_size(*a) <= most + 16 * 256
