@@ -128,7 +128,7 @@ struct LinCall {
 
 // Byte offsets of the workspace (one layout for the forward and the backward call).
 struct LinWs {
-    size_t slot, blk_start, run, gtot, gtot_head, X, Y, fin, rdot, cdot, dq32, dk32, part, total;
+    size_t slot, blk_start, run, gtot, X, Y, fin, rdot, cdot, dq32, dk32, part, total;
     int n_slots, nb, L;
     int nrun, n_runs;  // 0 where there are none
 };
