@@ -16,7 +16,8 @@ terms are off by 2^-21 at the very most, and by less than half of that in the me
 square; the sums over 16 x 8 tokens in the tensor cores, or 256 on the CUDA
 cores, and the carries add roundings of 2^-23 of a partial sum each, of which
 mostly independent ones come to less than sqrt(32) 2^-24: together below 2^-20,
-held to 2^-19.
+held to 2^-19.  (A state of which w c has lost its third bf16 term is off by
+more: test_linear_split.py.)
 
 The gradient of the decays at a token is a sum over up to 512 tokens of
 differences (R - C), each off by up to 2^-22 of its terms, while the sum itself
