@@ -33,10 +33,10 @@ __device__ __forceinline__ int block_scan(int x, int *warp_tot, int *total) {
 
 // One CTA.  Offsets are taken as their running maximum inside [0, rows], so
 // sequences never overlap and the slots always suffice.  `start` is scratch:
-// the sequences' first rows.  run (n_runs entries, may be none): the runs of the slots.
+// the sequences' first rows.  The runs of the slots are filled in where there are any.
 __global__ void __launch_bounds__(1024)
 plan_kernel(const int32_t *cu, Geo geo, int4 *slot,
-            int *blk_start, int *start, int2 *run) {
+            int *blk_start, int *start, Runs runs) {
     stream_order();
     __shared__ int wt[32];
     const int tid = threadIdx.x;
@@ -59,8 +59,8 @@ plan_kernel(const int32_t *cu, Geo geo, int4 *slot,
         nblk += add;
     }
     if (tid == 0) blk_start[geo.n_seq] = nblk;
-    for (int i = tid; i < geo.n_runs; i += 1024) run[i] = make_int2(-1, 0);
-    __syncthreads();  // read, and run overwritten, by other threads of this CTA below
+    for (int i = tid; i < runs.count; i += 1024) runs.of[i] = make_int2(-1, 0);
+    __syncthreads();  // read, and runs overwritten, by other threads of this CTA below
     for (int i = tid; i < geo.n_slots; i += 1024) {
         int4 r = make_int4(0, -1, 0, 0);
         if (i < nblk) {
@@ -73,8 +73,8 @@ plan_kernel(const int32_t *cu, Geo geo, int4 *slot,
             r = make_int4(t0, min(geo.L, start[2 * lo + 1] - t0), lo, b);
         }
         slot[i] = r;
-        if (geo.n_runs)
-            for (int j = 0, u = run_of(geo, r.x, i); j * kRunLen < r.y; ++j) run[u + j] = make_int2(i, j);
+        if (runs.count)
+            for (int j = 0, u = run_of(geo, runs, r.x, i); j * kRunLen < r.y; ++j) runs.of[u + j] = make_int2(i, j);
     }
 }
 
@@ -367,16 +367,15 @@ Geo lin_geo(const LinCall &c, const LinWs &w) {
     g.T = c.T; g.H = c.H; g.Hk = c.Hk; g.n_seq = c.cu ? c.n_seq : c.B; g.varlen = c.cu != nullptr;
     g.rows = c.B * c.T; g.L = w.L; g.nb = w.nb; g.n_slots = w.n_slots;
     g.gate_head = c.gate == GDR_GATE_HEAD;
-    g.nrun = w.nrun; g.n_runs = w.n_runs;
     return g;
 }
 
-cudaError_t lin_plan(const LinCall &c, const Geo &geo, const LinWs &w) {
+cudaError_t lin_plan(const LinCall &c, const Geo &geo, const LinWs &w, const Runs &runs) {
     if (!geo.varlen) return cudaSuccess;
     int *bs = (int *)(c.ws + w.blk_start);
     ProfToken tk = prof_begin(GDR_K_LIN_PLAN, c.st);
     const cudaError_t le = lin_launch(plan_kernel, dim3(1), 1024, 0, c.st, c.cu, geo, (int4 *)(c.ws + w.slot),
-                                      bs, bs + geo.n_seq + 1, (int2 *)(c.ws + w.run));
+                                      bs, bs + geo.n_seq + 1, runs);
     prof_end(tk, c.st);
     return le;
 }
@@ -384,7 +383,7 @@ cudaError_t lin_plan(const LinCall &c, const Geo &geo, const LinWs &w) {
 cudaError_t lin_scan(const LinCall &c, const Geo &geo, const LinWs &w, const LinScan *f, const LinScan *r) {
     if (!geo.n_slots && !(f && f->fin) && !(r && r->fin)) return cudaSuccess;
     const int nel = c.dk_ * c.dv_;
-    const Plan plan = {(const int4 *)(c.ws + w.slot), (const int *)(c.ws + w.blk_start), nullptr};
+    const Plan plan = {(const int4 *)(c.ws + w.slot), (const int *)(c.ws + w.blk_start)};
     const dim3 grid((unsigned)(geo.n_seq * geo.H), (unsigned)((nel / 4 + 255) / 256), f && r ? 2 : 1);
     ScanArgs a{}, b{};
     if (f) a = {f->X, f->gtot, f->init, f->fin};
@@ -398,7 +397,7 @@ cudaError_t lin_scan(const LinCall &c, const Geo &geo, const LinWs &w, const Lin
 cudaError_t lin_group_sum(const LinCall &c, const Geo &geo, const LinWs &w, const float *x, void *out,
                           int d) {
     if (!geo.n_slots) return cudaSuccess;
-    const Plan plan = {(const int4 *)(c.ws + w.slot), (const int *)(c.ws + w.blk_start), nullptr};
+    const Plan plan = {(const int4 *)(c.ws + w.slot), (const int *)(c.ws + w.blk_start)};
     const int rounds = (geo.L + kSumRows - 1) / kSumRows;
     const dim3 grid(geo.n_slots, rounds < 4096 ? rounds : 4096);
     ProfToken tk = prof_begin(GDR_K_LIN_SUM, c.st);

@@ -19,19 +19,22 @@ struct Geo {
     int gate_head;                      // g is [H]: one log-decay for all tokens
     int keep_empty;                     // an empty packed sequence has one block of no tokens
     int skip_single;                    // a sequence of one block takes its state from the caller's
-    int nrun, n_runs;                   // runs (kRunLen tokens) of a full block, of the call (see run_of)
 };
 
 // {first row, tokens, sequence, block}; a slot that no block fills has -1 tokens.
 struct Plan {
     const int4 *slot;      // packed batches only
     const int *blk_start;  // [n_seq + 1]: first slot of each sequence
-    const int2 *run;       // [n_runs]: {slot, run of the slot}, slot -1 where there is none
 };
 
 // Tokens of a run, the piece of a block over which the tensor-core path sums the
 // gradient of the decays before it starts again.
 constexpr int kRunLen = 512;
+
+struct Runs {
+    int block, count;  // of a full block; of the call
+    int2 *of;          // packed batches, [count]: {slot, run of the slot}, slot -1 where there is none
+};
 
 // Number of the first run of a slot whose first row is t0.  In a packed batch a
 // slot of n tokens has ceil(n / kRunLen) runs; consecutive slots start n rows and
@@ -40,8 +43,8 @@ constexpr int kRunLen = 512;
 // floor(rows / kRunLen) + n_slots, however the tokens are shared out.  (A full
 // block's runs for every slot took 12 GB for 256 sequences of 65,536 tokens, 16
 // heads and d 128.)
-__host__ __device__ __forceinline__ int run_of(const Geo &geo, int t0, int slot) {
-    return geo.varlen ? t0 / kRunLen + slot : slot * geo.nrun;
+__host__ __device__ __forceinline__ int run_of(const Geo &geo, const Runs &runs, int t0, int slot) {
+    return geo.varlen ? t0 / kRunLen + slot : slot * runs.block;
 }
 
 __device__ __forceinline__ int4 slot_of(const Geo &geo, const Plan &plan, int slot) {
@@ -128,14 +131,14 @@ struct LinCall {
 
 // Byte offsets of the workspace (one layout for the forward and the backward call).
 struct LinWs {
-    size_t slot, blk_start, run, gtot, X, Y, fin, rdot, cdot, dq32, dk32, part, total;
+    size_t slot, blk_start, gtot, X, Y, fin, rdot, cdot, dq32, dk32, part, total;
     int n_slots, nb, L;
-    int nrun, n_runs;  // 0 where there are none
 };
 LinWs lin_ws(int B, int T, int H, int Hk, int dk, int dv, int n_seq, bool varlen, bool bwd, int L,
              int dot_cols);
 gdr::lin::Geo lin_geo(const LinCall &c, const LinWs &w);
-cudaError_t lin_plan(const LinCall &c, const gdr::lin::Geo &geo, const LinWs &w);
+cudaError_t lin_plan(const LinCall &c, const gdr::lin::Geo &geo, const LinWs &w,
+                     const gdr::lin::Runs &runs = {});
 // States of the blocks carried over each sequence: X[slot] (the block's own
 // contribution) becomes the state that enters the block, from `init` on; `fin` (may
 // be NULL) receives the last state.  Forward in time (f), backward (r), or both in

@@ -427,7 +427,7 @@ int blocks_of(int d) { return (d + kNb - 1) / kNb; }
 size_t out_smem(int db) { return sizeof(float) * (size_t)(3 * kC * (db + 4) + 3 * kC * (kC + 4)); }
 
 Plan plan_of(const gdr_host::LinCall &c, const gdr_host::LinWs &w) {
-    return {(const int4 *)(c.ws + w.slot), (const int *)(c.ws + w.blk_start), nullptr};
+    return {(const int4 *)(c.ws + w.slot), (const int *)(c.ws + w.blk_start)};
 }
 
 gdr_host::LinWs simt_ws(const gdr_host::LinCall &c, bool bwd) {

@@ -95,6 +95,7 @@ struct TcArgs {
     // dots, forward: the state where a run starts, as the state's threads hold it; reverse: its
     // products with the gradient of that state, by warp
     float *bnd, *ydot;
+    Runs runs;
     int ha, hb, hc, he;  // heads of a, b, c, e
     int db, dc, ng;      // widths, column groups
     int tr;              // states are stored as the transpose of X
@@ -367,8 +368,8 @@ __device__ __forceinline__ void walk(unsigned int bid, const CUtensorMap &tm_a, 
     if (kChecked && !(chk_span(t0, len, geo.rows, err) && chk_span(slot, 1, geo.n_slots, err) &&
                       chk_tma(c0, 0, 2, p.dc, 1, err) &&
                       chk_true((smem_u32(sm) & 1023u) == 0 && len <= geo.L, err) &&
-                      (MODE != kOutDots || chk_span(run_of(geo, t0, slot), (len + kRunLen - 1) / kRunLen,
-                                                    geo.n_runs, err))))
+                      (MODE != kOutDots || chk_span(run_of(geo, p.runs, t0, slot),
+                                                    (len + kRunLen - 1) / kRunLen, p.runs.count, err))))
         return;
 
     if (tid == 0) {
@@ -852,11 +853,11 @@ __device__ __forceinline__ void walk(unsigned int bid, const CUtensorMap &tm_a, 
                         const int e = nch - cc;  // reverse: the chunk whose start this is
                         int at = -1;             // the run that starts there; at the block's end the next block's first
                         if (!REV) {
-                            if (cc % kRun == 0) at = run_of(geo, t0, slot) + cc / kRun;
+                            if (cc % kRun == 0) at = run_of(geo, p.runs, t0, slot) + cc / kRun;
                         } else if (cc > 0) {
-                            if (e % kRun == 0) at = run_of(geo, t0, slot) + e / kRun;
+                            if (e % kRun == 0) at = run_of(geo, p.runs, t0, slot) + e / kRun;
                         } else if (sl.w < nblk - 1) {
-                            at = run_of(geo, t0 + len, slot + 1);
+                            at = run_of(geo, p.runs, t0 + len, slot + 1);
                         }
                         if (at >= 0) {
                             const size_t u = ((size_t)at * geo.H + h) * p.ng + ng;
@@ -1197,6 +1198,7 @@ struct DgArgs {
     const float *fin, *dfin;    // S, dS at the sequences' ends, or dfin NULL (zero)
     float *dg, *part;
     int nel;
+    Runs runs;
 };
 __device__ __forceinline__ double warp_sum(double x) {
 #pragma unroll
@@ -1211,7 +1213,7 @@ dg_runs_kernel(DgArgs p, Geo geo, Plan plan) {
     __shared__ double tot[NW], inter[NW], red[NW];
     const int no = blockIdx.x / geo.H, h = blockIdx.x - no * geo.H;  // number of the run
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, grp = tid / kQ;
-    const int2 at_run = geo.varlen ? plan.run[no] : make_int2(no / geo.nrun, no % geo.nrun);
+    const int2 at_run = geo.varlen ? p.runs.of[no] : make_int2(no / p.runs.block, no % p.runs.block);
     const int slot = at_run.x;
     const int4 sl = slot < 0 ? make_int4(0, -1, 0, 0) : slot_of(geo, plan, slot);
     const int first = at_run.y * kRunLen, len = sl.y - first;  // tokens from the run's start
@@ -1223,7 +1225,7 @@ dg_runs_kernel(DgArgs p, Geo geo, Plan plan) {
     const bool more = len > kRunLen;  // the block goes on after the run
     double f = 0.0;
     if (more || sl.w < nblk - 1) {
-        const size_t u = (size_t)(more ? no + 1 : run_of(geo, sl.x + sl.y, slot + 1)) * geo.H + h;
+        const size_t u = (size_t)(more ? no + 1 : run_of(geo, p.runs, sl.x + sl.y, slot + 1)) * geo.H + h;
         if (tid < p.ny) f = p.ydot[u * p.ny + tid];
     } else if (p.dfin) {
         const size_t o = ((size_t)sl.z * geo.H + h) * p.nel;
@@ -1328,7 +1330,7 @@ int block_len(int n_seq, bool varlen, bool bwd, int T, int H, int ng, size_t nel
 
 struct TcWs {
     size_t slot, blk_start, run, gtot, gtot_rev, X, Y, fin, ri, ci, rp, cp, bnd, ydot, dq32, dk32, part, total;
-    int L, nb, n_slots, multi, nrun, n_runs;
+    int L, nb, n_slots, multi, run_blk, n_runs;
 };
 TcWs tc_ws(const LinCall &c, bool bwd) {
     TcWs w{};
@@ -1341,8 +1343,8 @@ TcWs tc_ws(const LinCall &c, bool bwd) {
     w.nb = (c.T + w.L - 1) / w.L;
     w.n_slots = varlen ? c.T / w.L + n_seq : c.B * w.nb;
     w.multi = w.nb > 1;
-    w.nrun = (w.L + kRunLen - 1) / kRunLen;
-    w.n_runs = !bwd ? 0 : varlen ? c.T / kRunLen + w.n_slots : w.n_slots * w.nrun;  // run_of
+    w.run_blk = (w.L + kRunLen - 1) / kRunLen;
+    w.n_runs = !bwd ? 0 : varlen ? c.T / kRunLen + w.n_slots : w.n_slots * w.run_blk;  // run_of
     const size_t sh = (size_t)w.n_slots * c.H;
     size_t o = 0;
     auto take = [&](size_t bytes) {
@@ -1378,9 +1380,6 @@ gdr_host::LinWs common_ws(const TcWs &w) {
     gdr_host::LinWs l{};
     l.slot = w.slot;
     l.blk_start = w.blk_start;
-    l.run = w.run;
-    l.nrun = w.nrun;
-    l.n_runs = w.n_runs;
     l.gtot = w.gtot;
     l.n_slots = w.n_slots;
     l.nb = w.nb;
@@ -1444,7 +1443,7 @@ cudaError_t lin_fwd_tc(const LinCall &c) {
     const LinWs l = common_ws(w);
     Geo geo = lin_geo(c, l);
     geo.keep_empty = geo.skip_single = 1;
-    const Plan plan = {(const int4 *)(c.ws + w.slot), (const int *)(c.ws + w.blk_start), (const int2 *)(c.ws + w.run)};
+    const Plan plan = {(const int4 *)(c.ws + w.slot), (const int *)(c.ws + w.blk_start)};
     Maps m;
     if (!make_maps(&m, c)) return cudaErrorUnknown;
     cudaError_t e;
@@ -1474,11 +1473,12 @@ cudaError_t lin_bwd_tc(const LinCall &c) {
     const LinWs l = common_ws(w);
     Geo geo = lin_geo(c, l);
     geo.keep_empty = geo.skip_single = 1;
-    const Plan plan = {(const int4 *)(c.ws + w.slot), (const int *)(c.ws + w.blk_start), (const int2 *)(c.ws + w.run)};
+    const Plan plan = {(const int4 *)(c.ws + w.slot), (const int *)(c.ws + w.blk_start)};
     Maps m;
     if (!make_maps(&m, c)) return cudaErrorUnknown;
     cudaError_t e;
-    if ((e = lin_plan(c, geo, l)) != cudaSuccess) return e;
+    const Runs runs{w.run_blk, w.n_runs, (int2 *)(c.ws + w.run)};
+    if ((e = lin_plan(c, geo, l, runs)) != cudaSuccess) return e;
     const bool shared = c.Hk < c.H;
     const __nv_bfloat16 *q = (const __nv_bfloat16 *)c.q, *k = (const __nv_bfloat16 *)c.k;
     float *X = (float *)(c.ws + w.X), *Y = (float *)(c.ws + w.Y), *fin = (float *)(c.ws + w.fin);
@@ -1520,6 +1520,7 @@ cudaError_t lin_bwd_tc(const LinCall &c) {
     p.dots = ri;
     p.bnd = (float *)(c.ws + w.bnd);
     p.ydot = (float *)(c.ws + w.ydot);
+    p.runs = runs;
     // pairs: CTAs for a (slot, head), as many as end soonest on 148 SMs, a start costing about as
     // much as one and a half chunks (B4 T4096 H16 d128: two, 191 us with dq's walks; four 200)
     const long units = (long)geo.n_slots * geo.H, most = w.L / kQ;
@@ -1570,14 +1571,14 @@ cudaError_t lin_bwd_tc(const LinCall &c) {
         if ((e = lin_group_sum(c, geo, l, (const float *)(c.ws + w.dk32), c.dk, c.dk_)) != cudaSuccess) return e;
     }
     DgArgs d{ri, ci, rp, cp, (const float *)(c.ws + w.ydot), 2 * groups(c.dk_), 2 * groups(c.dk_),
-             8 * groups(c.dk_), fin, c.dS_final, c.dg, part, c.dk_ * c.dv_};
+             8 * groups(c.dk_), fin, c.dS_final, c.dg, part, c.dk_ * c.dv_, runs};
     tk = prof_begin(GDR_K_LIN_GRAD, c.st);
-    e = lin_launch(dg_runs_kernel, dim3((unsigned)geo.n_runs * geo.H), kRunLen, 0, c.st, d, geo, plan);
+    e = lin_launch(dg_runs_kernel, dim3((unsigned)runs.count * geo.H), kRunLen, 0, c.st, d, geo, plan);
     prof_end(tk, c.st);
     if (e != cudaSuccess) return e;
     if (part) {
         Geo by_run = geo;  // one sum per run and head
-        by_run.n_slots = geo.n_runs;
+        by_run.n_slots = runs.count;
         if ((e = lin_dg_heads(c, by_run, part)) != cudaSuccess) return e;
     }
     return over ? launch_chain<true, kOut>(c, geo, plan, m.k, m.q, m.o, r, GDR_K_LIN_GRAD) : cudaSuccess;
