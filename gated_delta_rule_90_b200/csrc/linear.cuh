@@ -56,11 +56,13 @@ __device__ __forceinline__ int4 slot_of(const Geo &geo, const Plan &plan, int sl
 // First statement of every kernel of these calls but decode: the kernel is started
 // (lin_launch) when the blocks of the one before it in the stream have ended, and waits
 // here until that one's results are visible.  What is saved is the part of a launch
-// before this point, 2 to 5 us at each kernel: the gradients of 2 x 1,500 tokens with a
-// decay for each head take 75 us in place of 89, the packed forward pass 357 in place
-// of 368.  To start the next kernel earlier, when this one's last blocks have begun
-// (griddepcontrol.launch_dependents), takes more: waiting blocks hold the shared memory
-// that this kernel's are still to use (gradients of a batch 443 us, 430 before, 424 so).
+// before this point, 2 to 5 us at each kernel: measured in turn on one GPU, calls one after
+// another on the same inputs, the gradients of 2 x 1,500 tokens with a decay for each head
+// took 75 us in place of 89, the packed forward pass 357 in place of 368 (other GPUs and
+// new inputs for each call: up to 12 % more on both sides).  To start the next kernel
+// earlier, when this one's last blocks have begun (griddepcontrol.launch_dependents), takes
+// more: waiting blocks hold the shared memory that this kernel's are still to use (gradients
+// of a batch, in turn: 443 us, 430 with plain launches, 424 so).
 // Pointers that reach a kernel's loads are not __restrict__ in its arguments, and no
 // load is of the read-only kind: such a load may be moved up across the wait.
 __device__ __forceinline__ void stream_order() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

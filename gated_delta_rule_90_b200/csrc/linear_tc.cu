@@ -330,9 +330,9 @@ __device__ __forceinline__ float row_factor(float li) {
 //
 // Loops over columns are rolled where they can be: the five roles' unrolled code
 // did not fit the instruction caches, and warps waited for instructions most of
-// the time (forward, B4 T4096 H16 d128: 225 us unrolled, 151 us rolled; 93 us now).
+// the time (forward, B4 T4096 H16 d128: 225 us unrolled, 151 us rolled; 88 to 95 us now).
 // Bound by the latencies of the chain of hand-offs of a chunk (5,500 cycles), not by
-// a pipe: issue slots 52 %, tensor 35 %, shared memory 46 %, DRAM 31 % busy at that size.
+// a pipe: issue slots 52 %, tensor 35 %, shared memory 45 %, DRAM 32 % busy at that size.
 template <bool REV, int MODE>
 __device__ __forceinline__ void walk(unsigned int bid, const CUtensorMap &tm_a, const CUtensorMap &tm_b,
                                      const CUtensorMap &tm_c, const TcArgs &p, const Geo &geo, const Plan &plan,
@@ -936,7 +936,7 @@ __device__ __forceinline__ void walk(unsigned int bid, const CUtensorMap &tm_a, 
 // q_l . dq_l) and column sums (of k_m . dk_m), fp32.  Both factors are products
 // of inputs, so no operand is rounded.  The column sums are the row sums of the
 // transposed products, which the tensor cores form as well: 32 more MMAs cost
-// less than summing over lanes.  Reads q, k, v, dout once.  B4 T4096 H16 d128: 69 us
+// less than summing over lanes.  Reads q, k, v, dout once.  B4 T4096 H16 d128, alone: 69 us
 // (its bytes 41 us), with 8 warps for the sums 125.
 struct PairArgs {
     const float *g;
@@ -1299,8 +1299,16 @@ size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 // one walk to an SM, a chunk of one 2.6 us and 5 us to start (three walks, 10 us and
 // 15 us for the gradient), without outputs 1.9 us and 4 us (measured; T 8192, H 4,
 // d 128 forward: 164 us in one piece, 35 us in 16; B 4, T 4096, H 16: 94 us in one,
-// 146 us in two).  Of packed sequences the host does not know the lengths: those
-// longer than one and a half times an SM's share of all tokens are cut.
+// 146 us in two).  The constants are those of d 128; at d 64, where a chunk takes less,
+// the pieces that they choose took (best of 1, 2, 4, 8, 16 pieces in brackets): forward
+// T 8192, H 4 32 us (35), B 4, T 4096, H 16 87 us (87); gradients 78 us (65), 282 us
+// (253), B 2, T 1500, H 8 70 us (56).  Of packed sequences the host does not know the
+// lengths: those longer than one and a half times an SM's share of all tokens are cut.
+// d 128, in us, at three quarters of a share, at one and a half, at three, and uncut: one
+// sequence of 8,192 tokens, H 4, forward 59, 48, 67, 169, gradients 134, 127, 133, 464;
+// 16 sequences of 65,536, H 16, forward 378, 377, 376, 366; gradients of 9 of 8,191,
+// H 16 275, 270, 274, 260.  d 64: 37, 37, 46, 171; 83, 91, 86, 453; 285, 211, 211, 204;
+// 193, 175, 168, 166.
 int block_len(int n_seq, bool varlen, bool bwd, int T, int H, int ng, size_t nel) {
     const double sms = 148.0;
     const int ch = (T + kQ - 1) / kQ;
@@ -1522,7 +1530,7 @@ cudaError_t lin_bwd_tc(const LinCall &c) {
     p.ydot = (float *)(c.ws + w.ydot);
     p.runs = runs;
     // pairs: CTAs for a (slot, head), as many as end soonest on 148 SMs, a start costing about as
-    // much as one and a half chunks (B4 T4096 H16 d128: two, 191 us with dq's walks; four 200)
+    // much as one and a half chunks (gradients of B4 T4096 H16 d128: one 463 us, two 410, four 414)
     const long units = (long)geo.n_slots * geo.H, most = w.L / kQ;
     long split = 1;
     double least = 1e30;
