@@ -527,7 +527,7 @@ def gdr_fwd_linear(q, k, v, g, S0=None, *, cu_seqlens=None, out=None, S_final=No
     Like every call of this module it works on the tensors' memory: results do
     not require gradients, whatever the inputs do.  For training call it and
     gdr_bwd_linear from the two sides of a ``torch.autograd.Function``."""
-    if len(q.shape) != 4 or len(v.shape) != 4:
+    if q.ndim != 4 or v.ndim != 4:
         _linear_rank(4, q=q, v=v)
     B, T = q.shape[:2]
     n_seq, varlen = _linear_cu(cu_seqlens, B)
@@ -557,7 +557,7 @@ def gdr_decode_step_linear(q, k, v, g, S, *, out=None, stream=None) -> torch.Ten
     """Linear attention decode of one token per sequence, updating ``S``
     [N,H,d_v,d_k] in place: q, k [N,H_k,d_k], v [N,H,d_v], g [N,H] or [H];
     returns out [N,H,d_v]."""
-    if len(q.shape) != 3 or len(v.shape) != 3:
+    if q.ndim != 3 or v.ndim != 3:
         _linear_rank(3, q=q, v=v)
     N = q.shape[0]
     dev, dtype, gate, H, H_k, d_k, d_v = _linear_args(q, k, v, g, (
@@ -587,7 +587,7 @@ def gdr_bwd_linear(q, k, v, g, dout, S0=None, dS_final=None, *, cu_seqlens=None,
     dq, dk and dv of the tokens' type, dg and dS0 fp32.  It takes the forward's
     inputs as they were (keep S0 where S_final was written over it) and nothing
     of its results."""
-    if len(q.shape) != 4 or len(v.shape) != 4:
+    if q.ndim != 4 or v.ndim != 4:
         _linear_rank(4, q=q, v=v)
     B, T = q.shape[:2]
     n_seq, varlen = _linear_cu(cu_seqlens, B)
